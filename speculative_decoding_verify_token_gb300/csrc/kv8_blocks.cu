@@ -428,7 +428,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
                         float m = -INFINITY;
 #pragma unroll
                         for (int e = p * 16; e < p * 16 + 16; e += 2) m = fmaxf(fmaxf(m, x[e]), x[e + 1]);
-                        mx = fmaxf(mx, fmaf(m, fabsf(pm[p].x) * qs, pm[p].y));
+                        mx = fmaxf(mx, fmaf(m, kv8_factor(pm[p].x, qs), pm[p].y));
                     }
                     if (__any_sync(FULL, mx > ref + 8.0f)) {
                         const bool move = mx > ref + 8.0f;
@@ -464,7 +464,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
                         float h[16];
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            const float vs = pm[2 * c + p].z, sc = fabsf(pm[2 * c + p].x) * qs;
+                            const float vs = pm[2 * c + p].z, sc = kv8_factor(pm[2 * c + p].x, qs);
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
                                 const int k = c * 32 + p * 16 + e;

@@ -176,6 +176,11 @@ __device__ __forceinline__ float kv8_lg2(float x) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// What raw scores of a page are multiplied by, never below the smallest normal number: masked scores are
+// -inf, and -inf times an underflowed factor (a zero query's 2^-118 and a zero page's 2^-64) would be NaN.
+// Finite raw scores are below 2^24: where this factor replaces a smaller one, the score is below 2^-102 anyway.
+__device__ __forceinline__ float kv8_factor(float key_scale, float row) { return fmaxf(fabsf(key_scale) * row, 1.1754944e-38f); }
+
 // Barrier of the row kernel's 256 softmax threads, true if any of them passes pred != 0.
 __device__ __forceinline__ int kv8_rows_any(int pred) {
     int r;

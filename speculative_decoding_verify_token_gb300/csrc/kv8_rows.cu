@@ -426,7 +426,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
 #pragma unroll
                         for (int e = p * 16; e < p * 16 + 16; e += 2) m = fmaxf(fmaxf(m, x[e]), x[e + 1]);
                         const float4 pm = tm[2 * (c0 + u) + p];
-                        mx = fmaxf(mx, fmaf(m, fabsf(pm.x) * rq, pm.y));
+                        mx = fmaxf(mx, fmaf(m, kv8_factor(pm.x, rq), pm.y));
                     }
                 }
                 if (__any_sync(FULL, mx > ref + KR_MOVE)) {
@@ -463,7 +463,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const float4 pm = tm[2 * c + p];
-                        const float vs = pm.z, sc = fabsf(pm.x) * rq;
+                        const float vs = pm.z, sc = kv8_factor(pm.x, rq);
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             float2 w[2];
