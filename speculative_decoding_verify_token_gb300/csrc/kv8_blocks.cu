@@ -40,13 +40,6 @@ template <int D> struct KbCfg {
     static constexpr size_t SMEM = 1024 + 2 * (size_t)QBYTES + KB_NK * TILE + KB_NV * TILE + KB_NV * 2 * TILE;
 };
 
-// fp16 values, K-major over the keys without swizzle: core matrices of 8 dimensions x 8 keys,
-// 128 bytes apart along the dimensions, D * 16 bytes apart along the keys.
-template <int D> __device__ __forceinline__ uint64_t kb_desc_v16(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(D * 16 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
-           ((uint64_t)1 << 46);
-}
-
 template <int D>
 __global__ void __launch_bounds__(KB_THREADS, 1)
 kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_ml, Kv8Run* runs, bool after) {
@@ -231,7 +224,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
                         }
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t vd = kb_desc_v16<D>(vring + (i % KB_NV) * 2 * C::TILE) + u * 4 * (2 * D * 16 >> 4);
+                        const uint64_t vd = kv8_desc_v16<D>(vring + (i % KB_NV) * 2 * C::TILE) + u * 4 * (2 * D * 16 >> 4);
                         if (kv8_elect()) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
@@ -297,12 +290,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
                     uint4 w = *reinterpret_cast<const uint4*>(src + p * 16 * D);
                     const int keys = s.len - (t * 8 + p) * 16;
                     if (keys < 16 || meta[ms][p].x < 0.0f) kv8_keep(w, meta[ms][p].x < 0.0f ? 0 : keys);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t h[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) kv8_widen4(u[e], h[2 * e], h[2 * e + 1]);
-                    *reinterpret_cast<uint4*>(dst + (2 * p) * D * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(dst + (2 * p + 1) * D * 16) = make_uint4(h[4], h[5], h[6], h[7]);
+                    kv8_widen16<D>(w, dst + (2 * p) * D * 16);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();

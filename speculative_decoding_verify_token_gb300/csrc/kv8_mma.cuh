@@ -1,6 +1,5 @@
 // Device pieces shared by the attention kernels of the 8-bit paged cache: operand and
-// instruction descriptors, tensor-memory loads, the two-term e4m3 splits of queries and
-// probabilities.
+// instruction descriptors, tensor-memory loads, the two-term e4m3 split of queries, values widened to fp16.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,15 +22,6 @@ __device__ __forceinline__ void kv8_mma(uint32_t d_tmem, uint64_t a, uint64_t b,
         :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
-// The same with A in tensor memory (four codes a column); lanes of D whose bit is set in `off`
-// are not written.
-__device__ __forceinline__ void kv8_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, const uint32_t (&off)[4], uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}"
-        :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]) : "memory");
-}
-
 // K-major rows of D bytes (keys, queries): 128-byte swizzle for D = 128, 64-byte for D = 64;
 // groups of eight rows follow each other.
 template <int D> __device__ __forceinline__ uint64_t kv8_desc_rows(uint32_t addr) {
@@ -39,10 +29,10 @@ template <int D> __device__ __forceinline__ uint64_t kv8_desc_rows(uint32_t addr
            ((uint64_t)1 << 46) | ((uint64_t)(D == 128 ? 2 : 4) << 61);
 }
 
-// Values, K-major over the keys without swizzle: core matrices of 8 dimensions x 16 tokens,
-// 128 bytes apart along the dimensions, a page's block (16 D bytes) apart along the keys.
-template <int D> __device__ __forceinline__ uint64_t kv8_desc_values(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(16 * D >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
+// Values widened to fp16, K-major over the keys without swizzle: core matrices of 8 dimensions x 8 keys,
+// 128 bytes apart along the dimensions, D * 16 bytes apart along the keys.
+template <int D> __device__ __forceinline__ uint64_t kv8_desc_v16(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(D * 16 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
            ((uint64_t)1 << 46);
 }
 
@@ -99,6 +89,14 @@ __device__ __forceinline__ void kv8_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem,
         :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
+// The same; lanes of D whose bit is set in `off` are not written.
+__device__ __forceinline__ void kv8_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, const uint32_t (&off)[4], uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]) : "memory");
+}
+
 __device__ __forceinline__ void kv8_tmem_ld16(uint32_t taddr, float (&v)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
@@ -129,9 +127,10 @@ __device__ __forceinline__ void kv8_tmem_st32(uint32_t taddr, const float* v) {
 }
 __device__ __forceinline__ void kv8_tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two probabilities in fp16 (never infinite: past its range only by the rounding of enormous scores).
 __device__ __forceinline__ uint32_t kv8_half2(float lo, float hi) {
     uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
@@ -262,6 +261,16 @@ __device__ __forceinline__ void kv8_keep(uint4& w, int keep) {
 __device__ __forceinline__ void kv8_widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// The 16 codes of a dimension in a page as fp16, into the two core matrices that hold its first and last eight keys.
+template <int D> __device__ __forceinline__ void kv8_widen16(uint4 w, uint8_t* dst) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kv8_widen4(u[e], h[2 * e], h[2 * e + 1]);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(dst + D * 16) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
 // The two attention kernels, and the join of the groups that their runs share.  The second of a

@@ -9,21 +9,23 @@
 //  * S = Q K^T (tcgen05 kind::f8f6f4).  K are the cache's codes; q = (hi + lo) 2^e per row, two
 //    e4m3 terms that hold a bf16's 8 bits exactly (elements below 2^-9 of the row's largest
 //    lose bits below 2^-17 of it);
-//  * with x = s log2(e): p = 2^(x - ref + 5), the sum adds p, P = p x value scale = hi + lo in
-//    e4m3 (8 bits from 2^-8 of the row's largest on, then down to 2^-15 of it), so that P V
-//    needs only the codes.  ref follows the largest x + log2(value scale) when that passes it by 3
-//    (P <= 2^8), which after the first tiles is rare; then the row's output is rescaled;
-//  * O += P V (f8f6f4): P lies over the scores in tensor memory, each 32 keys' terms over their
-//    own scores; a product of 32 keys leaves the lanes of the other copies alone; V are the codes.
+//  * with x = s log2(e): p = 2^(x - ref + 12), the sum adds p, P = p x value scale in fp16 (11 bits
+//    down to 2^-26 of the row's largest, then in steps of 2^-36 of it).  ref follows the largest x +
+//    log2(value scale) when that passes it by 3 (P <= 2^15), which after the first tiles is rare; then
+//    the row's output is rescaled.  In an 8-bit format the probabilities of a long context's many small
+//    keys do not survive beside a large one: two e4m3 terms end at 2^-15 of it, and with 90% of the sum on
+//    one key of 16k the other 10% came out up to half too small (short of them the sum, which is fp32, is not);
+//  * O += P V (kind::f16): P lies over the scores in tensor memory, each 32 keys' over their own
+//    scores; a product of 16 keys leaves the lanes of the other copies alone; V are the codes widened to
+//    fp16 (exact) by the warps that prepare the queries.
 // Two groups of four warps take alternate tiles with outputs of their own; at the end of a
 // run's part of a group the copies and both outputs are added through shared memory.
 // What it replaced (32 verify passes of up to 16k keys): the running maximum of every tile over
-// lanes that held keys, 580 us; a vote per tile instead, values widened to fp16 for
-// one-term probabilities, 212 us, bound by the latency of some 4,600 warp instructions a tile
-// (this form has 1,100 to 1,900).  Now 135 us for those (74% of the copy rate, the tensor pipe
+// lanes that held keys, 580 us; a vote per tile instead, 212 us, bound by the latency of some 4,600 warp
+// instructions a tile (this form has 1,700 to 2,300).  Now 135 us for those (74% of the copy rate, the tensor pipe
 // 53% busy), 59 us for 5 rows of 128k keys, 76 us for 48 decodes of D = 64.
 // Warps: 0-3 and 4-7 softmax, 8 copies keys, 9 copies values and writes the pages' factors, 10 and
-// 11 issue the MMAs of the two groups, 12-15 prepare the queries of the next group of rows.
+// 11 issue the MMAs of the two groups, 12-15 widen values and prepare the queries of the next group of rows.
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cmath>
@@ -34,7 +36,7 @@ namespace sv {
 
 constexpr int KR_THREADS = 512;
 constexpr int KR_WIN = 4;               // tiles of a window: a lane of the copy warps to each page
-constexpr float KR_LEAD = 5.0f;         // exponent of P at the reference
+constexpr float KR_LEAD = 12.0f;        // exponent of P at the reference
 constexpr float KR_MOVE = 3.0f;         // how far a maximum passes the reference before it moves
 
 // Tensor memory columns of a group: scores (and probabilities), output.
@@ -43,8 +45,10 @@ constexpr uint32_t KR_S = 0, KR_O = 256;
 template <int D> struct KrCfg {
     static constexpr uint32_t TILE = KV8_TILE * D;           // bytes of a tile's keys (values)
     static constexpr uint32_t QBYTES = 32768;                // hi rows, lo rows; 32 outputs of 256 lanes
-    static constexpr int NST = D == 128 ? 4 : 8;             // ring slots of keys, and of values
-    static constexpr size_t SMEM = 1024 + 2 * QBYTES + 2 * (size_t)NST * TILE;
+    static constexpr int NK = D == 128 ? 3 : 8;              // ring slots of keys,
+    static constexpr int NC = D == 128 ? 2 : 4;              // of values as codes
+    static constexpr int NV = D == 128 ? 2 : 3;              // and as fp16
+    static constexpr size_t SMEM = 1024 + 2 * QBYTES + (size_t)(NK + NC + 2 * NV) * TILE;
 };
 
 // Lanes of one copy of a group of R rows.
@@ -65,7 +69,7 @@ __global__ void __launch_bounds__(KR_THREADS, 1)
 kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_ml, Kv8Run* runs, bool after) {
     using C = KrCfg<D>;
     extern __shared__ uint8_t kr_smem[];
-    __shared__ __align__(8) uint64_t k_full[C::NST], k_empty[C::NST], v_full[C::NST], v_empty[C::NST];
+    __shared__ __align__(8) uint64_t k_full[C::NK], k_empty[C::NK], c_full[C::NC], c_empty[C::NC], v_full[C::NV], v_empty[C::NV];
     __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], m_full[2], m_empty[2], turn[2], done_bar[2];
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
@@ -78,10 +82,16 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // barriers, a lane to each slot, before anything is waited for
     if (warp == 11) {
-        if (lane < C::NST) {
+        if (lane < C::NK) {
             mbar_init(smem_u32(&k_full[lane]), 1);
             mbar_init(smem_u32(&k_empty[lane]), 1);
-            mbar_init(smem_u32(&v_full[lane]), 1);
+        }
+        if (lane < C::NC) {
+            mbar_init(smem_u32(&c_full[lane]), 1);
+            mbar_init(smem_u32(&c_empty[lane]), 4);
+        }
+        if (lane < C::NV) {
+            mbar_init(smem_u32(&v_full[lane]), 4);
             mbar_init(smem_u32(&v_empty[lane]), 1);
         }
         if (lane < 2) {
@@ -133,7 +143,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
     }
     const uint32_t base = (smem_u32(kr_smem) + 1023u) & ~1023u;
     uint8_t* gbase = kr_smem + (base - smem_u32(kr_smem));
-    const uint32_t kring = base + 2 * C::QBYTES, vring = kring + C::NST * C::TILE;
+    const uint32_t kring = base + 2 * C::QBYTES, cring = kring + C::NK * C::TILE, vring = cring + C::NC * C::TILE;
     if (warp == 10) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :: "r"(smem_u32(&tmem_sh)), "r"(512u) : "memory");
@@ -149,22 +159,23 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
     auto wait = [&](uint64_t& bar, uint32_t parity) { return kv8_wait_warp(bar, parity, abort_flag); };
 
     if (warp >= 12) {
-        // ---- queries as hi + lo terms: 128 / span threads to a row, each with its share of the
-        // dimensions, which it writes to every copy.  A buffer is free when the softmax is done
-        // with the group two before ----
-        const int tid = threadIdx.x - 384;
-        uint32_t seg = 0;
-#pragma unroll 1
-        while (ok && walk.next(a, s)) {
-            if (seg >= 2) ok = wait(q_free[seg & 1], (seg >> 1) - 1);
-            if (kv8_query_any(!ok)) {        // (and q_top is read)
-                ok = false;
-                break;
-            }
-            const int R = s.n * G, span = kr_span(R), r = tid & (span - 1), t = r / G;
+        // ---- values: codes to fp16, zeros behind the last key; in between the queries of the next group.
+        // A group's queries come before its values, the next one's as soon as their buffer is free: when
+        // the softmax is done with the group two before, whose values are all behind us.  A warp
+        // whose wait gave up goes on voting, so that all four leave together ----
+        const int tid = threadIdx.x - 384, d = tid % D;
+        constexpr int STEP = 128 / D;                // D = 64: each half of the threads takes every other page
+        KrWalk qw = walk;
+        Kv8Seg qseg;
+        bool qmore = qw.next(a, qseg);
+        uint32_t seg = 0, at = 0, i = 0;             // groups prepared, the group and the tile that are widened
+        // queries as hi + lo terms: 128 / span threads to a row, each with its share of the dimensions,
+        // which it writes to every copy
+        auto prepare = [&]() {
+            const int R = qseg.n * G, span = kr_span(R), r = tid & (span - 1), t = r / G;
             const int cnt = D / 8 * span / 128, c0 = tid / span * cnt;          // chunks of eight dimensions: 2, 4, 8 or 16
-            const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (long long)(s.row0 + t) * a.q_stride +
-                                                             (size_t)(s.h * G + r - t * G) * D) + c0;
+            const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (long long)(qseg.row0 + t) * a.q_stride +
+                                                             (size_t)(qseg.h * G + r - t * G) * D) + c0;
             uint32_t top = 0;
 #pragma unroll 4
             for (int c = 0; c < cnt; ++c) top = max(top, kv8_top_exponent(r < R ? qp[c] : make_uint4(0, 0, 0, 0)));
@@ -195,6 +206,53 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&q_full[seg & 1]));
             ++seg;
+            qmore = qw.next(a, qseg);
+        };
+#pragma unroll 1
+        while (walk.next(a, s)) {
+            bool now = seg == at;                    // this group's queries are not there yet
+#pragma unroll 1
+            for (int t = s.t0; t <= s.t1; ++t) {
+                if (now || (qmore && seg == at + 1 && t > s.t0)) {
+                    // (a vote also says that q_top is read)
+                    bool free_ = true;
+                    if (seg >= 2) {
+                        if (now) ok = ok && wait(q_free[seg & 1], (seg >> 1) - 1);
+                        else free_ = mbar_test(smem_u32(&q_free[seg & 1]), ((seg >> 1) - 1) & 1);
+                    }
+                    const bool no = kv8_query_any(!ok || !free_) != 0;
+                    if (!no) prepare();
+                    else if (now) {
+                        ok = false;
+                        break;
+                    }
+                    now = false;
+                }
+                if (t == s.t1) break;
+                const int cs = (int)(i % C::NC), vs = (int)(i % C::NV);
+                ok = ok && wait(c_full[cs], i / C::NC) && (i < C::NV || wait(v_empty[vs], i / C::NV - 1));
+                if (!ok) abort_flag = 1;
+                else {
+                    const uint8_t* src = gbase + (cring - base) + cs * C::TILE + d * 16;
+                    uint8_t* dst = gbase + (vring - base) + vs * 2 * C::TILE + d * 16;
+#pragma unroll 2
+                    for (int p = tid / D; p < 8; p += STEP) {
+                        uint4 w = *reinterpret_cast<const uint4*>(src + p * 16 * D);
+                        const int keys = s.len - (t * 8 + p) * 16;
+                        if (keys < 16) kv8_keep(w, keys);        // codes behind the last key: anything, and 0 x NaN is NaN
+                        kv8_widen16<D>(w, dst + (2 * p) * D * 16);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&v_full[vs]));
+                        mbar_arrive(smem_u32(&c_empty[cs]));
+                    }
+                }
+                ++i;
+            }
+            if (now) break;
+            ++at;
         }
         if (!ok) abort_flag = 1;
     } else if (warp == 8 || warp == 9) {
@@ -202,9 +260,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // when its tile comes.  Eight copies of a warp take it some 600 clocks, so that little else may
         // be done tile by tile: the pages' factors go out a window at a time ----
         const bool vals = warp == 9;
-        uint64_t* full = vals ? v_full : k_full;
-        uint64_t* empty = vals ? v_empty : k_empty;
-        const uint32_t ring = vals ? vring : kring;
+        uint64_t* full = vals ? c_full : k_full;
+        uint64_t* empty = vals ? c_empty : k_empty;
+        const uint32_t ring = vals ? cring : kring, NS = vals ? C::NC : C::NK;
         const uint64_t pol = policy_evict_first();
         const uint32_t mine = (uint32_t)(lane & 7) * 16 * D;          // this lane's page in a tile
         uint32_t i = 0, win = 0;                 // tiles and windows of the run
@@ -247,8 +305,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
                 }
                 if (w == 2) sc_ahead = factors(ahead);
                 const unsigned pages = have >> (w * 8) & 0xffu;
-                const int sl = (int)(i % C::NST);
-                if (i >= C::NST) ok = wait(empty[sl], i / C::NST - 1);
+                const int sl = (int)(i % NS);
+                if (i >= NS) ok = wait(empty[sl], i / NS - 1);
                 if (!ok) break;
                 const uint32_t fb = smem_u32(&full[sl]);
                 if (vals && pages != 0xffu) {
@@ -271,7 +329,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // no copy may still be landing when the block leaves
         if (lane == 0)
 #pragma unroll 1
-            for (uint32_t j = i > (uint32_t)C::NST ? i - C::NST : 0; j < i; ++j) kv8_wait(full[j % C::NST], (j / C::NST) & 1);
+            for (uint32_t j = i > NS ? i - NS : 0; j < i; ++j) kv8_wait(full[j % NS], (j / NS) & 1);
     } else if (warp == 10 || warp == 11) {
         // ---- MMA issuers, one per group of softmax warps (tile i belongs to group i % 2).  They take
         // turns, tile by tile, so that the waits of one hide behind the MMAs of the other without
@@ -279,9 +337,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // tile, a single one 1,850, of which the MMAs are 1,024).  A tile's scores follow the
         // product of tile i - 2, whose probabilities they overwrite: MMAs of one thread run in
         // order.  The whole warp walks, so that the descriptors stay uniform; one lane issues.  Keys
-        // and values are waited for ahead of the probabilities.  A product of 32 keys writes only
+        // and values are waited for ahead of the probabilities.  A product of 16 keys writes only
         // the lanes of the copy that has them (what the others hold there is their scores) ----
-        const uint32_t id_s = kv8_idesc(128), id_o = kv8_idesc(D);
+        const uint32_t id_s = kv8_idesc(128), id_o = kv8_idesc_f16(D);
         const int g = warp == 10 ? 0 : 1;
         KrWalk pw = walk;
         Kv8Seg ps;
@@ -301,13 +359,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
             }
         };
         auto scores = [&]() {                // by the elected lane
-            const uint64_t kd = kv8_desc_rows<D>(kring + (i % C::NST) * C::TILE), qd = kv8_desc_rows<D>(base + (seg & 1) * C::QBYTES);
+            const uint64_t kd = kv8_desc_rows<D>(kring + (i % C::NK) * C::TILE), qd = kv8_desc_rows<D>(base + (seg & 1) * C::QBYTES);
 #pragma unroll
             for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
                     kv8_mma(tmem + KR_S + g * 128, qd + (lo * 128 * D >> 4) + k * 2, kd + k * 2, id_s, lo | k);
-            mma_commit(smem_u32(&k_empty[i % C::NST]));
+            mma_commit(smem_u32(&k_empty[i % C::NK]));
             mma_commit(smem_u32(&s_full[g]));
         };
         step(g);
@@ -323,28 +381,26 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
 #pragma unroll 1
             for (int pt = ps.t0; pt < ps.t1; ++pt, ++j) {
                 if ((int)(j & 1) != g) continue;
-                const int sl = (int)(j % C::NST);
+                const int sl = (int)(j % C::NV);
                 // the queries of a group two after the product's need that group's end: not waited for
                 // before its last product
                 const bool with = more && (t - s.t0 >= 2 || __all_sync(FULL, mbar_test(smem_u32(&q_full[seg & 1]), (seg >> 1) & 1)));
-                ok = wait(v_full[sl], j / C::NST) && (!more || wait(k_full[i % C::NST], i / C::NST)) && wait(p_full[g], j >> 1) && (j == 0 || wait(turn[g], g ? j >> 1 : (j >> 1) - 1));
+                ok = wait(v_full[sl], j / C::NV) && (!more || wait(k_full[i % C::NK], i / C::NK)) && wait(p_full[g], j >> 1) && (j == 0 || wait(turn[g], g ? j >> 1 : (j >> 1) - 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t vd = kv8_desc_values<D>(vring + sl * C::TILE);
+                const uint64_t vd = kv8_desc_v16<D>(vring + sl * 2 * C::TILE);
                 const uint32_t keep = pt - ps.t0 >= 2 ? 1u : 0u;      // not its group's first tile
                 const int span = kr_span(ps.n * G);
                 if (kv8_elect()) {
 #pragma unroll
-                    for (int lo = 0; lo < 2; ++lo)
+                    for (int k = 0; k < 8; ++k) {
+                        // lanes not written: all but the span that has keys 16 k ..
+                        uint32_t off[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            // lanes not written: all but the span that has keys 32 k ..
-                            uint32_t off[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) off[q] = q * 32 / span == k * 32 / span ? 0u : 0xffffffffu;
-                            kv8_mma_ts(tmem + KR_O + g * 128, tmem + KR_S + g * 128 + k * 32 + lo * 8, vd + (k * 32 * D >> 4), id_o, off,
-                                       lo || (k * 32 & (span - 1)) ? 1u : keep);
-                        }
+                        for (int q = 0; q < 4; ++q) off[q] = q * 32 / span == k * 16 / span ? 0u : 0xffffffffu;
+                        kv8_mma_f16_ts(tmem + KR_O + g * 128, tmem + KR_S + g * 128 + k / 2 * 32 + (k & 1) * 8, vd + k * (2 * D * 16 >> 4), id_o, off,
+                                       k * 16 & (span - 1) ? 1u : keep);
+                    }
                     mma_commit(smem_u32(&v_empty[sl]));
                     if (pt + 2 >= ps.t1) mma_commit(smem_u32(&o_done[g]));
                     if (with) scores();
@@ -459,44 +515,26 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
                 for (int u = nchk - 1; u >= 0; --u) {
                     const int c = c0 + u;
                     if (u < nchk - 1) load(c);           // the last chunk is still here
-                    float h[16];                         // 8 words of hi terms, 8 of lo terms
+                    float h[16];
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const float4 pm = tm[2 * c + p];
                         const float vs = pm.z, sc = kv8_factor(pm.x, rq);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            float2 w[2];
-#pragma unroll
-                            for (int f = 0; f < 2; ++f) {
-                                const float2 y = kv8_fma2(make_float2(x[p * 16 + e + 2 * f], x[p * 16 + e + 2 * f + 1]), make_float2(sc, sc), make_float2(sub, sub));
-                                const float2 z = make_float2(kv8_exp2(y.x), kv8_exp2(y.y));
-                                sum = kv8_add2(sum, z);
-                                w[f] = kv8_mul2(z, make_float2(vs, vs));
-                            }
-                            uint32_t hi, lo;
-                            kv8_split4(w[0], w[1], hi, lo);
-                            h[p * 4 + e / 4] = __uint_as_float(hi);
-                            h[8 + p * 4 + e / 4] = __uint_as_float(lo);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 y = kv8_fma2(make_float2(x[p * 16 + e], x[p * 16 + e + 1]), make_float2(sc, sc), make_float2(sub, sub));
+                            const float2 z = make_float2(kv8_exp2(y.x), kv8_exp2(y.y));
+                            sum = kv8_add2(sum, z);
+                            const float2 w = kv8_mul2(z, make_float2(vs, vs));
+                            h[p * 8 + e / 2] = __uint_as_float(kv8_half2(w.x, w.y));
                         }
                     }
                     kv8_tmem_st16(ts + c * 32, h);
                 }
                 l += sum.x + sum.y;
-                if ((t + 1) * KV8_TILE > s.len && (s.len & 15) && j < D) {
-                    // value codes behind the last key: anything, and 0 x NaN is NaN
-                    ok = kv8_wait(v_full[i % C::NST], (i / C::NST) & 1);
-                    uint4* vt = reinterpret_cast<uint4*>(gbase + (vring - base) + (i % C::NST) * C::TILE +
-                                                         ((s.len - t * KV8_TILE) >> 4) * 16 * D + j * 16);
-                    uint4 w = *vt;
-                    kv8_keep(w, s.len & 15);
-                    *vt = w;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
                 kv8_tmem_wait_st();
                 tc_fence_before();
-                ok = __all_sync(FULL, ok) != 0;
-                if (!ok) break;
+                __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&p_full[grp]));
                     if (last_of) mbar_arrive(smem_u32(&m_empty[win & 1]));

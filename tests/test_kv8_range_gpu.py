@@ -107,3 +107,76 @@ def test_scale_zero_with_small_numbers(kv8, size, n):  # noqa: F811
         lse = torch.empty(n, hq, device=DEV)
         out = kv8.attention(q, pool, scales, table, ints([0, n]), ints([L]), scale=scale, lse=lse)
         check(out, lse, q, pool, scales, range(21), [L - n + t for t in range(n)], scale)
+
+
+# ---- a key that holds most of the softmax ---------------------------------------------------
+
+def sink_cache(g, L, hkv, D, at, sink_value):
+    """One context of L keys that all sequences read: keys near zero but the one at `at`, which
+    is 1 along every dimension; values 1 + noise, that key's `sink_value`."""
+    pages = -(-L // 16)
+    k = torch.randn(L, 1, hkv * D, generator=g, device=DEV).view(L, hkv, D) * 2.0 ** -8
+    v = 1 + 0.25 * torch.randn(L, hkv, D, generator=g, device=DEV)
+    k[at], v[at] = 1.0, sink_value
+    return pages, k, v
+
+
+@pytest.mark.parametrize("L,D", [(2048, 128), (8192, 64), (16384, 128), (32768, 64), (32760, 128), (131072, 128)])
+@pytest.mark.parametrize("n", [1, 9, 32, 40])          # 4, 36 and 128 rows per kv head, and a prompt chunk
+def test_one_key_with_most_of_the_softmax(kv8, L, D, n):  # noqa: F811
+    """An attention sink before a long flat context.  19 sequences of 8 kv heads are as many groups as
+    there are runs, so that each run holds a group from end to end."""
+    g = torch.Generator(device=DEV).manual_seed(L + n)
+    B, hkv, G = 19, 8, 4
+    for at, sink_value in ((0, 0.0), (L // 2, 1.0)):
+        pages, k, v = sink_cache(g, L, hkv, D, at, sink_value)
+        pool, scales = kv8.new_cache(pages, hkv, D)
+        table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1)
+        kv8.append(pool, scales, table, ints([0, L]), ints([L]), k, v)
+        for share in (0.5, 0.9, 0.99):
+            # q . k / sqrt(D) of the sink against the others' zero: its share of the sum
+            gap = math.log(share / (1 - share) * (L - 1))
+            q = (torch.full((B * n, hkv * G, D), gap / D ** 0.5, device=DEV)
+                 + 0.02 * torch.randn(B * n, hkv * G, D, generator=g, device=DEV)).bfloat16()
+            lse = torch.empty(B * n, hkv * G, device=DEV)
+            out = kv8.attention(q, pool, scales, table.expand(B, pages).contiguous(), ints(np.arange(B + 1) * n), ints([L] * B), lse=lse)
+            for b in (0, 7):
+                for t in sorted({0, n - 1}):
+                    r = slice(b * n + t, b * n + t + 1)
+                    check(out[r], lse[r], q[r], pool, scales, range(pages), [L - n + t])
+
+
+@pytest.mark.parametrize("n", [1, 9, 32, 200])
+def test_one_key_with_most_of_the_softmax_split(kv8, n):  # noqa: F811
+    """The same for one sequence, whose groups are split over many runs and joined."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    hkv, G, L, D = 2, 4, 30000, 128
+    pages, k, v = sink_cache(g, L, hkv, D, 5, 0.0)
+    pool, scales = kv8.new_cache(pages, hkv, D)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1)
+    kv8.append(pool, scales, table, ints([0, L]), ints([L]), k, v)
+    for share in (0.5, 0.9, 0.99):
+        gap = math.log(share / (1 - share) * (L - 1))
+        q = torch.full((n, hkv * G, D), gap / D ** 0.5, device=DEV).bfloat16()
+        lse = torch.empty(n, hkv * G, device=DEV)
+        out = kv8.attention(q, pool, scales, table, ints([0, n]), ints([L]), lse=lse)
+        check(out[-1:], lse[-1:], q[-1:], pool, scales, range(pages), [L - 1])
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(8, 2, 128), (5, 1, 64), (16, 1, 128)])
+@pytest.mark.parametrize("seqs", list(base.ATT))
+def test_attention_without_a_floor(kv8, seqs, hq, hkv, D):  # noqa: F811
+    """Ordinary and sharp softmaxes over pages of scales octaves apart, to the same bound."""
+    rng = np.random.default_rng(len(seqs) + hq + D)
+    for amp, spread in ((1.5, 2), (20.0, 2), (1.0, 9)):
+        rs, kv, table, pool, scales = base.make_cache(rng, base.ATT[seqs], hkv, D, True, spread)
+        q = torch.from_numpy(rng.standard_normal((int(rs[-1]), hq, D)) * amp).to(torch.bfloat16).to(DEV)
+        pd, sd = torch.from_numpy(pool).to(DEV), torch.from_numpy(scales).to(DEV)
+        lse = torch.empty(q.shape[:2], device=DEV)
+        out = kv8.attention(q, pd, sd, ints(table), ints(rs), ints(kv), lse=lse)
+        for b, (n, L) in enumerate(base.ATT[seqs]):
+            r = slice(int(rs[b]), int(rs[b + 1]))
+            if n and L:
+                check(out[r], lse[r], q[r], pd, sd, table[b], [L - n + t for t in range(n)])
+            else:
+                assert (out[r] == 0).all() and torch.isneginf(lse[r]).all()
