@@ -523,9 +523,9 @@ int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int B, int max_
  * zeros.  q and out: bf16, row r, head i at q + r * q_stride + i * head_dim (strides in
  * elements, multiples of 8; 16-byte aligned); lse (may be NULL): float32 [n_rows][n_q_heads],
  * the natural logarithm of the softmax's denominator, -inf for rows without a key.  Keys and
- * values enter as codes times scale, queries exactly, the probabilities times value scale in two e4m3
- * terms (8 bits, to within 2^-15 of the row's largest) or, above 128 rows per kv head of a
- * sequence, in fp16; sums and softmax statistics are fp32.  Scales are positive, in
+ * values enter as codes times scale, queries exactly, the probabilities times value scale in fp16
+ * (11 bits, to within 2^-37 of the row's largest, above 128 rows per kv head of a sequence
+ * 2^-32); sums and softmax statistics are fp32.  Scales are positive, in
  * [2^-64, 2^120]; value codes of positions below kv_len are not NaN (as spec_kv8_append
  * leaves them).  n_q_heads is a multiple of n_kv_heads, at most 64 per kv head.
  * workspace: spec_kv8_attention_workspace_bytes(...) bytes, 256-byte aligned, contents

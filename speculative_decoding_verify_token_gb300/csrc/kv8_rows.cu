@@ -22,8 +22,9 @@
 // run's part of a group the copies and both outputs are added through shared memory.
 // What it replaced (32 verify passes of up to 16k keys): the running maximum of every tile over
 // lanes that held keys, 580 us; a vote per tile instead, 212 us, bound by the latency of some 4,600 warp
-// instructions a tile (this form has 1,700 to 2,300).  Now 135 us for those (74% of the copy rate, the tensor pipe
-// 53% busy), 59 us for 5 rows of 128k keys, 76 us for 48 decodes of D = 64.
+// instructions a tile (this form has 1,700 to 2,300).  Now 152 us for those (66% of the copy rate),
+// 64 us for 5 rows of 128k keys, 81 us for 48 decodes of D = 64; with the e4m3 probabilities, whose products
+// need no widened values, it was 136, 59 and 76.
 // Warps: 0-3 and 4-7 softmax, 8 copies keys, 9 copies values and writes the pages' factors, 10 and
 // 11 issue the MMAs of the two groups, 12-15 widen values and prepare the queries of the next group of rows.
 #include <cuda_bf16.h>
@@ -35,6 +36,7 @@
 namespace sv {
 
 constexpr int KR_THREADS = 512;
+constexpr int KR_WIDEN = 128;           // threads that widen values
 constexpr int KR_WIN = 4;               // tiles of a window: a lane of the copy warps to each page
 constexpr float KR_LEAD = 12.0f;        // exponent of P at the reference
 constexpr float KR_MOVE = 3.0f;         // how far a maximum passes the reference before it moves
@@ -45,9 +47,9 @@ constexpr uint32_t KR_S = 0, KR_O = 256;
 template <int D> struct KrCfg {
     static constexpr uint32_t TILE = KV8_TILE * D;           // bytes of a tile's keys (values)
     static constexpr uint32_t QBYTES = 32768;                // hi rows, lo rows; 32 outputs of 256 lanes
-    static constexpr int NK = D == 128 ? 3 : 8;              // ring slots of keys,
-    static constexpr int NC = D == 128 ? 2 : 4;              // of values as codes
-    static constexpr int NV = D == 128 ? 2 : 3;              // and as fp16
+    static constexpr int NK = D == 128 ? 3 : 5;              // ring slots of keys,
+    static constexpr int NC = D == 128 ? 2 : 5;              // of values as codes
+    static constexpr int NV = D == 128 ? 2 : 4;              // and as fp16
     static constexpr size_t SMEM = 1024 + 2 * QBYTES + (size_t)(NK + NC + 2 * NV) * TILE;
 };
 
@@ -88,10 +90,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         }
         if (lane < C::NC) {
             mbar_init(smem_u32(&c_full[lane]), 1);
-            mbar_init(smem_u32(&c_empty[lane]), 4);
+            mbar_init(smem_u32(&c_empty[lane]), KR_WIDEN / 32);
         }
         if (lane < C::NV) {
-            mbar_init(smem_u32(&v_full[lane]), 4);
+            mbar_init(smem_u32(&v_full[lane]), KR_WIDEN / 32);
             mbar_init(smem_u32(&v_empty[lane]), 1);
         }
         if (lane < 2) {
@@ -163,8 +165,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // A group's queries come before its values, the next one's as soon as their buffer is free: when
         // the softmax is done with the group two before, whose values are all behind us.  A warp
         // whose wait gave up goes on voting, so that all four leave together ----
-        const int tid = threadIdx.x - 384, d = tid % D;
-        constexpr int STEP = 128 / D;                // D = 64: each half of the threads takes every other page
+        const int tid = threadIdx.x - 384;
+        constexpr int NL = 8 * D / KR_WIDEN;         // 16-byte pieces of a thread
         KrWalk qw = walk;
         Kv8Seg qseg;
         bool qmore = qw.next(a, qseg);
@@ -230,24 +232,30 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
                 }
                 if (t == s.t1) break;
                 const int cs = (int)(i % C::NC), vs = (int)(i % C::NV);
-                ok = ok && wait(c_full[cs], i / C::NC) && (i < C::NV || wait(v_empty[vs], i / C::NV - 1));
+                ok = ok && wait(c_full[cs], i / C::NC);
+                // all pieces at once, and the codes' slot given back before they are converted: one warp a scheduler has
+                // nothing but its own latency to hide (two pages at a time, the slot at the end: 166 us for 152)
+                uint4 w[NL];
+                if (ok) {
+                    const uint4* src = reinterpret_cast<const uint4*>(gbase + (cring - base) + cs * C::TILE) + tid;
+#pragma unroll
+                    for (int k = 0; k < NL; ++k) w[k] = src[k * KR_WIDEN];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&c_empty[cs]));
+                    if (i >= C::NV) ok = wait(v_empty[vs], i / C::NV - 1);
+                }
                 if (!ok) abort_flag = 1;
                 else {
-                    const uint8_t* src = gbase + (cring - base) + cs * C::TILE + d * 16;
-                    uint8_t* dst = gbase + (vring - base) + vs * 2 * C::TILE + d * 16;
-#pragma unroll 2
-                    for (int p = tid / D; p < 8; p += STEP) {
-                        uint4 w = *reinterpret_cast<const uint4*>(src + p * 16 * D);
-                        const int keys = s.len - (t * 8 + p) * 16;
-                        if (keys < 16) kv8_keep(w, keys);        // codes behind the last key: anything, and 0 x NaN is NaN
-                        kv8_widen16<D>(w, dst + (2 * p) * D * 16);
-                    }
+                    const int left = s.len - t * KV8_TILE;
+                    if (left < KV8_TILE)                     // codes behind the last key: anything, and 0 x NaN is NaN
+#pragma unroll
+                        for (int k = 0; k < NL; ++k) kv8_keep(w[k], left - (k * KR_WIDEN + tid) / D * 16);
+                    uint8_t* dst = gbase + (vring - base) + vs * 2 * C::TILE;
+#pragma unroll
+                    for (int k = 0; k < NL; ++k) kv8_widen16<D>(w[k], dst + ((k * KR_WIDEN + tid) / D * 2 * D + (k * KR_WIDEN + tid) % D) * 16);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&v_full[vs]));
-                        mbar_arrive(smem_u32(&c_empty[cs]));
-                    }
+                    if (lane == 0) mbar_arrive(smem_u32(&v_full[vs]));
                 }
                 ++i;
             }
