@@ -33,25 +33,30 @@ __device__ __forceinline__ int kr_tiles(const Kv8Attn& a, int b, int& slot, int&
     return n > 0 && (long long)n * (a.hq / a.hkv) <= KR_ROWS ? (len + KV8_TILE - 1) / KV8_TILE : 0;
 }
 
-// Units (of some 0.2 us) of a tile and of the rest of a group of R rows.
+// Units (of some 0.2 us) of a tile and of the rest of a group of R rows, mostly the wait for its queries.  Batches of
+// 32 sequences to 16k, D = 128: a tile takes 0.84, 0.98 and 1.4 us, the rest of a group 4.4, 6.2 and 8.1 to 9.3;
+// 48 sequences to 8k, D = 64: 0.7, 0.96 and 1.2, and 2.7 to 3.2.  The extras are those whose runs end closest to
+// each other (32 verify passes: 152 us with 12, 22 and 26 for both, 142 with these; 48 decodes 80 and 72).
 __device__ __forceinline__ int kr_weight(int R) { return R <= 32 ? 4 : (R <= 64 ? 5 : 6); }
-__device__ __forceinline__ int kr_extra(int R) { return R <= 32 ? 12 : (R <= 64 ? 22 : 26); }
+template <int D> __device__ __forceinline__ int kr_extra(int R) {
+    return D == 64 ? (R <= 32 ? 18 : (R <= 64 ? 26 : 32)) : (R <= 32 ? 24 : (R <= 64 ? 36 : 46));
+}
 
 // Units of a kv head of n > 0 tokens, and the first tile of a run that begins at unit u of it.
-__device__ __forceinline__ int kr_group(const Kv8Attn& a, int n, int tiles) {
+template <int D> __device__ __forceinline__ int kr_group(const Kv8Attn& a, int n, int tiles) {
     const int R = n * (a.hq / a.hkv);
-    return tiles * kr_weight(R) + kr_extra(R);
+    return tiles * kr_weight(R) + kr_extra<D>(R);
 }
-__device__ __forceinline__ int kr_tile_of(const Kv8Attn& a, int n, int u) {
+template <int D> __device__ __forceinline__ int kr_tile_of(const Kv8Attn& a, int n, int u) {
     const int R = n * (a.hq / a.hkv), w = kr_weight(R);
-    return max(u - kr_extra(R) + w - 1, 0) / w;
+    return max(u - kr_extra<D>(R) + w - 1, 0) / w;
 }
 
 // Units of all kv heads of sequence b.
-__device__ __forceinline__ long long kr_units(const Kv8Attn& a, int b) {
+template <int D> __device__ __forceinline__ long long kr_units(const Kv8Attn& a, int b) {
     int slot, row0, n, len;
     const int tiles = kr_tiles(a, b, slot, row0, n, len);
-    return tiles ? (long long)kr_group(a, n, tiles) * a.hkv : 0;
+    return tiles ? (long long)kr_group<D>(a, n, tiles) * a.hkv : 0;
 }
 
 // ---- the blocks list ----
@@ -206,7 +211,7 @@ __device__ __forceinline__ void kv8_note(Kv8Run& r, const Kv8Seg& s, bool& begun
 }
 
 // Walks the run [pos, end) of the rows list; b holds pos, its first unit is index base.
-struct KrWalk {
+template <int D> struct KrWalk {
     long long left;                 // units of the run still to come
     long long at;                   // offset in sequence b's units (of all kv heads)
     int b, tiles, slot, row0, n, len;
@@ -218,19 +223,19 @@ struct KrWalk {
 #pragma unroll 1
         while (left > 0) {
 #pragma unroll 1
-            while (tiles == 0 || at >= (long long)kr_group(a, n, tiles) * a.hkv) {
+            while (tiles == 0 || at >= (long long)kr_group<D>(a, n, tiles) * a.hkv) {
                 at = 0;
                 if (++b >= a.B) return false;
                 tiles = kr_tiles(a, b, slot, row0, n, len);
             }
-            const int units = kr_group(a, n, tiles), h = (int)(at / units), u0 = (int)(at - (long long)h * units);
+            const int units = kr_group<D>(a, n, tiles), h = (int)(at / units), u0 = (int)(at - (long long)h * units);
             const int u1 = left < units - u0 ? u0 + (int)left : units;
             at += u1 - u0;
             left -= u1 - u0;
             s.b = b; s.rb = 0; s.tiles = tiles; s.slot = slot; s.row0 = row0; s.n = n; s.len = len;
             s.h = h;
-            s.t0 = kr_tile_of(a, n, u0);
-            s.t1 = kr_tile_of(a, n, u1);
+            s.t0 = kr_tile_of<D>(a, n, u0);
+            s.t1 = kr_tile_of<D>(a, n, u1);
             if (s.t1 > s.t0) return true;
         }
         return false;

@@ -22,9 +22,9 @@
 // run's part of a group the copies and both outputs are added through shared memory.
 // What it replaced (32 verify passes of up to 16k keys): the running maximum of every tile over
 // lanes that held keys, 580 us; a vote per tile instead, 212 us, bound by the latency of some 4,600 warp
-// instructions a tile (this form has 1,700 to 2,300).  Now 152 us for those (66% of the copy rate),
-// 64 us for 5 rows of 128k keys, 81 us for 48 decodes of D = 64; with the e4m3 probabilities, whose products
-// need no widened values, it was 136, 59 and 76.
+// instructions a tile.  Now 142 us for those (70% of the copy rate),
+// 61 us for 5 rows of 128k keys, 72 us for 48 decodes of D = 64; with two-term e4m3 probabilities, whose products
+// need no widened values, 136, 59 and 76.
 // Warps: 0-3 and 4-7 softmax, 8 copies keys, 9 copies values and writes the pages' factors, 10 and
 // 11 issue the MMAs of the two groups, 12-15 widen values and prepare the queries of the next group of rows.
 #include <cuda_bf16.h>
@@ -120,7 +120,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
     long long fbase;
     const long long total = kv8_find(
         a.B, scan,
-        [&](int b) { return kr_units(a, b); },
+        [&](int b) { return kr_units<D>(a, b); },
         [&](long long t) { return kv8_run_begin(t, blockIdx.x); }, fb, fbase);
     // rows without a key: those before the first and behind the last sequence, and the first n - len
     // of a sequence of len < n positions; spread over the blocks
@@ -137,7 +137,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
             for (int r = 0; r < min(n, n - len); ++r) kr_zero_row(a, row0 + r, D, threadIdx.x, KR_THREADS);
         }
     }
-    KrWalk walk;
+    KrWalk<D> walk;
     walk.start(a, kv8_run_begin(total, blockIdx.x), kv8_run_begin(total, blockIdx.x + 1), fb, fbase);
     if (walk.left <= 0) {        // no run for this block
         kv8_finish(after);
@@ -167,7 +167,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // whose wait gave up goes on voting, so that all four leave together ----
         const int tid = threadIdx.x - 384;
         constexpr int NL = 8 * D / KR_WIDEN;         // 16-byte pieces of a thread
-        KrWalk qw = walk;
+        KrWalk<D> qw = walk;
         Kv8Seg qseg;
         bool qmore = qw.next(a, qseg);
         uint32_t seg = 0, at = 0, i = 0;             // groups prepared, the group and the tile that are widened
@@ -349,7 +349,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // the lanes of the copy that has them (what the others hold there is their scores) ----
         const uint32_t id_s = kv8_idesc(128), id_o = kv8_idesc_f16(D);
         const int g = warp == 10 ? 0 : 1;
-        KrWalk pw = walk;
+        KrWalk<D> pw = walk;
         Kv8Seg ps;
         uint32_t i = 0, seg = 0;             // this group's next tile to score, its group of rows
         int t = 0;
