@@ -558,7 +558,7 @@ extern "C" int spec_kv8_plan(int B, int max_pages, int max_rows, int free_capaci
                kv_len_out, held_out, reinterpret_cast<long long*>(slots), positions, row_seq, status};
     const int blocks = std::max(1, std::min((max_rows + PLAN_THREADS - 1) / PLAN_THREADS, 152));
     const size_t smem = sizeof(int) * (4 * (size_t)B + 1);
-    if (smem > 48 * 1024) {
+    if (B > 2048) {                     // (from 32 KB on: the 48 KB that need no opting in hold the static arrays too)
         const cudaError_t e = cudaFuncSetAttribute(kv8_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)(sizeof(int) * (4 * PLAN_MAX_B + 1)));
         if (e != cudaSuccess) return set_error(SPEC_E_CUDA, "plan attributes: %s", cudaGetErrorString(e));
