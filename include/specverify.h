@@ -523,7 +523,8 @@ int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int B, int max_
  * zeros.  q and out: bf16, row r, head i at q + r * q_stride + i * head_dim (strides in
  * elements, multiples of 8; 16-byte aligned); lse (may be NULL): float32 [n_rows][n_q_heads],
  * the natural logarithm of the softmax's denominator, -inf for rows without a key.  Keys and
- * values enter as codes times scale, queries exactly, the probabilities times value scale in fp16
+ * values enter as codes times scale, queries exactly (elements below 2^-13 of a row's largest to
+ * within 2^-21 of it), the probabilities times value scale in fp16
  * (11 bits, to within 2^-37 of the row's largest, above 128 rows per kv head of a sequence
  * 2^-32); sums and softmax statistics are fp32.  Scales are positive, in
  * [2^-64, 2^120]; value codes of positions below kv_len are not NaN (as spec_kv8_append

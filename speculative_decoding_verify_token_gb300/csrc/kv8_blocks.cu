@@ -8,7 +8,7 @@
 // rows (token-major, G query heads each), the M of the products, that share the key and value
 // tiles.  Per tile of 128 keys and block:
 //  * S = Q K^T (tcgen05 kind::f8f6f4): the cache's key codes as they are, q = hi + lo in
-//    e4m3 (exact for bf16, see the rows kernel), accumulated in tensor memory;
+//    e4m3 and e5m2 (exact for bf16, see the rows kernel), accumulated in tensor memory;
 //  * one thread per row, 64 keys at a time: p = 2^(s log2(e) - ref + 7), summed in fp32, and P =
 //    p x value scale in fp16 (11 bits; at most 2^15) over the scores.  The row's reference
 //    moves only when its maximum of s log2(e) + log2(value scale) passes it by 2^8 (then the
@@ -175,7 +175,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
             // probabilities read by it: MMAs of one thread run in order.  The whole warp walks, so
             // that the descriptors stay uniform; one lane issues.  A slot of keys or values is free
             // after both issuers ----
-            const uint32_t id_s = kv8_idesc(64), id_o = kv8_idesc_f16(D);
+            const uint32_t id_s = kv8_idesc(64, 0), id_lo = kv8_idesc(64, 1), id_o = kv8_idesc_f16(D);
             const int blk = warp == 13 ? 0 : 1;
             uint32_t i = 0, seg = 0, done = 0;       // tiles of the run; groups and tiles of this block
             uint32_t turns = 0;                      // this issuer's turns
@@ -199,7 +199,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
                     for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k)
-                            kv8_mma(tmem + blk * 128 + u * 64, qd + (lo * 128 * D >> 4) + k * 2, kd + k * 2, id_s, lo | k);
+                            kv8_mma(tmem + blk * 128 + u * 64, qd + (lo * 128 * D >> 4) + k * 2, kd + k * 2, lo ? id_lo : id_s, lo | k);
                     mma_commit(smem_u32(&s_full[blk][u]));
                     if (u) mma_commit(smem_u32(&k_empty[j % KB_NK]));
                 };

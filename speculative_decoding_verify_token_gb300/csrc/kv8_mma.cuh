@@ -1,5 +1,5 @@
 // Device pieces shared by the attention kernels of the 8-bit paged cache: operand and
-// instruction descriptors, tensor-memory loads, the two-term e4m3 split of queries, values widened to fp16.
+// instruction descriptors, tensor-memory loads, the two-term split of queries, values widened to fp16.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -10,9 +10,9 @@
 
 namespace sv {
 
-// kind::f8f6f4, D fp32, A and B e4m3, both K-major, M = 128, N = n.
-__device__ __forceinline__ uint32_t kv8_idesc(int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+// kind::f8f6f4, D fp32, A e4m3 or e5m2 (the second query term), B e4m3, both K-major, M = 128, N = n.
+__device__ __forceinline__ uint32_t kv8_idesc(int n, int e5m2) {
+    return (1u << 4) | ((uint32_t)e5m2 << 7) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
 __device__ __forceinline__ void kv8_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -217,26 +217,28 @@ __device__ __forceinline__ uint32_t kv8_top_exponent(uint4 w) {
 }
 __device__ __forceinline__ int kv8_exponent_of(uint32_t top) { return max((int)top - 127 - 7, -118); }
 
-// Four numbers (at most 448) as hi + lo in e4m3.  The remainder is taken in half precision (11
-// bits, 7 more than hi), where it is exact.
+// Four numbers (at most 448) as hi in e4m3 + lo in e5m2.  The remainder is taken in half precision (11
+// bits, 7 more than hi), where it is exact.  Of a number of 8 bits it is at most 8 of its last units, which 3
+// bits hold, and e5m2 ends at 2^-16, 2^7 below e4m3: a second term in e4m3 lost bits of elements from
+// 2^-9 of the row's largest on, which decide the scores of queries with an outlier channel.
 __device__ __forceinline__ void kv8_split4(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
     asm("{\n\t.reg .b32 h, g;\n\t.reg .b16 x, y, u, v;\n\t"
         "cvt.rn.f16x2.f32 h, %3, %2;\n\t"
         "cvt.rn.satfinite.e4m3x2.f16x2 x, h;\n\t"
         "cvt.rn.f16x2.e4m3x2 g, x;\n\t"
         "sub.rn.f16x2 h, h, g;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 u, h;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 u, h;\n\t"
         "cvt.rn.f16x2.f32 h, %5, %4;\n\t"
         "cvt.rn.satfinite.e4m3x2.f16x2 y, h;\n\t"
         "cvt.rn.f16x2.e4m3x2 g, y;\n\t"
         "sub.rn.f16x2 h, h, g;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 v, h;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 v, h;\n\t"
         "mov.b32 %0, {x, y};\n\tmov.b32 %1, {u, v};\n\t}"
         : "=r"(hi), "=r"(lo) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
 }
 
-// x 2^-e as hi + lo, two e4m3 terms each (NaN or infinite x: NaN).  x has 8 bits, so that half
-// precision holds x 2^-e < 2^8 as it is, but for bits below 2^-24.
+// x 2^-e as hi + lo (NaN or infinite x: NaN).  x has 8 bits, so that half precision holds x 2^-e < 2^8
+// as it is, but for bits below 2^-24.  Exact from 2^-6 on (2^-13 of 2^7), off by 2^-14 at most below.
 __device__ __forceinline__ void kv8_split8(float (&x)[8], int e, uint2& hi, uint2& lo) {
     const float f = __uint_as_float((uint32_t)(127 - e) << 23);
     if (e == kv8_exponent_of(255))          // the exponent of infinities and NaN

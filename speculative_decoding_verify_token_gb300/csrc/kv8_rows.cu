@@ -6,9 +6,9 @@
 // group's rows in 4, 2 or 1 copies (up to 32, 64, 128 rows), and copy k of a row takes only
 // every k-th part of a tile's 128 keys: all lanes work however few rows there are, one
 // thread has one row, and nothing is reduced over lanes until the end.  Per tile:
-//  * S = Q K^T (tcgen05 kind::f8f6f4).  K are the cache's codes; q = (hi + lo) 2^e per row, two
-//    e4m3 terms that hold a bf16's 8 bits exactly (elements below 2^-9 of the row's largest
-//    lose bits below 2^-17 of it);
+//  * S = Q K^T (tcgen05 kind::f8f6f4).  K are the cache's codes; q = (hi + lo) 2^e per row, hi in
+//    e4m3 and lo in e5m2, which hold a bf16's 8 bits exactly (elements below 2^-13 of the row's
+//    largest are off by up to 2^-21 of it);
 //  * with x = s log2(e): p = 2^(x - ref + 12), the sum adds p, P = p x value scale in fp16 (11 bits
 //    down to 2^-26 of the row's largest, then in steps of 2^-36 of it).  ref follows the largest x +
 //    log2(value scale) when that passes it by 3 (P <= 2^15), which after the first tiles is rare; then
@@ -347,7 +347,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // order.  The whole warp walks, so that the descriptors stay uniform; one lane issues.  Keys
         // and values are waited for ahead of the probabilities.  A product of 16 keys writes only
         // the lanes of the copy that has them (what the others hold there is their scores) ----
-        const uint32_t id_s = kv8_idesc(128), id_o = kv8_idesc_f16(D);
+        const uint32_t id_s = kv8_idesc(128, 0), id_lo = kv8_idesc(128, 1), id_o = kv8_idesc_f16(D);
         const int g = warp == 10 ? 0 : 1;
         KrWalk<D> pw = walk;
         Kv8Seg ps;
@@ -372,7 +372,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
             for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
-                    kv8_mma(tmem + KR_S + g * 128, qd + (lo * 128 * D >> 4) + k * 2, kd + k * 2, id_s, lo | k);
+                    kv8_mma(tmem + KR_S + g * 128, qd + (lo * 128 * D >> 4) + k * 2, kd + k * 2, lo ? id_lo : id_s, lo | k);
             mma_commit(smem_u32(&k_empty[i % C::NK]));
             mma_commit(smem_u32(&s_full[g]));
         };

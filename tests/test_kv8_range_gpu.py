@@ -182,3 +182,24 @@ def test_attention_without_a_floor(kv8, seqs, hq, hkv, D):  # noqa: F811
                 check(out[r], lse[r], q[r], pd, sd, table[b], [L - n + t for t in range(n)])
             else:
                 assert (out[r] == 0).all() and torch.isneginf(lse[r]).all()
+
+
+# ---- query rows with an outlier -------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [3, 140])
+@pytest.mark.parametrize("size", [100.0, 4096.0])
+def test_queries_with_an_outlier_channel(kv8, size, n, D):  # noqa: F811
+    """One channel of the queries is far larger than the others and the keys are zero there: the
+    others decide the scores."""
+    rng = np.random.default_rng(n + D)
+    hq, hkv, L = 8, 2, 500
+    rs, kv, table, pool, scales = base.make_cache(rng, [(n, L)], hkv, D)
+    pool[:, :, 0][:, :, ref.key_index(D)[:, 3]] = 0
+    q = rng.standard_normal((n, hq, D)) * 2
+    q[:, :, 3] = size * np.sign(q[:, :, 3])
+    q = torch.from_numpy(q).to(torch.bfloat16).to(DEV)
+    pd, sd = torch.from_numpy(pool).to(DEV), torch.from_numpy(scales).to(DEV)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = kv8.attention(q, pd, sd, ints(table), ints(rs), ints(kv), lse=lse)
+    check(out, lse, q, pd, sd, table[0], [L - n + t for t in range(n)])
