@@ -240,6 +240,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
                     const uint4* src = reinterpret_cast<const uint4*>(gbase + (cring - base) + cs * C::TILE) + tid;
 #pragma unroll
                     for (int k = 0; k < NL; ++k) w[k] = src[k * KR_WIDEN];
+                    // these loads before the copy that the slot is given back to: without the fence it landed while
+                    // they were still on their way, and some dimensions of a tile had another tile's values
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&c_empty[cs]));
                     if (i >= C::NV) ok = wait(v_empty[vs], i / C::NV - 1);
