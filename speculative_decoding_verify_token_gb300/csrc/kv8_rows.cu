@@ -396,7 +396,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
                 // the queries of a group two after the product's need that group's end: not waited for
                 // before its last product
                 const bool with = more && (t - s.t0 >= 2 || __all_sync(FULL, mbar_test(smem_u32(&q_full[seg & 1]), (seg >> 1) & 1)));
-                ok = wait(v_full[sl], j / C::NV) && (!more || wait(k_full[i % C::NK], i / C::NK)) && wait(p_full[g], j >> 1) && (j == 0 || wait(turn[g], g ? j >> 1 : (j >> 1) - 1));
+                // (the turn ahead of the keys: a slot whose tiles go to both issuers can be waited for only when its
+                // phase before is complete, and the other issuer has waited for that one before it passes the turn)
+                ok = wait(v_full[sl], j / C::NV) && (j == 0 || wait(turn[g], g ? j >> 1 : (j >> 1) - 1)) &&
+                     (!more || wait(k_full[i % C::NK], i / C::NK)) && wait(p_full[g], j >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = kv8_desc_v16<D>(vring + sl * 2 * C::TILE);
