@@ -341,19 +341,19 @@ int spec_kv_trim(spec_ctx* ctx, int B, const int32_t* seq_ids, int K, const int3
 int spec_seq_len(spec_ctx* ctx, int seq_id, int32_t* out_len);
 
 /* Wait for the context's stream, then report the device-side status: SPEC_E_TIMEOUT when
- * a bounded wait inside a kernel (a tensor-core GEMM's pipeline barriers; each gives up
- * after 2 s) gave up since the context was created.  The
+ * a bounded wait inside a kernel (the pipeline barriers of a tensor-core GEMM or attention,
+ * with the 8-bit cache too; each gives up after 2 s) gave up since the context was created.  The
  * kernel then skipped the rest of its work, so results since then are unreliable; the
  * status is sticky and the context must be destroyed.  SPEC_E_CUDA on a stream error.
  * (No counterpart on the pages: the library's own failure reporting.) */
 int spec_sync(spec_ctx* ctx);
 
 /* Check of the failure path above: launch one bounded wait (the GEMM kernels' own wait
- * helper, with a budget of budget_ms milliseconds, 1..2000) on a barrier that nothing
- * completes.  The wait runs out, records SPEC_E_TIMEOUT in the context's device status
+ * helper, with the 8-bit cache its attention's, with a budget of budget_ms milliseconds,
+ * 1..2000) on a barrier that nothing completes.  The wait runs out, records SPEC_E_TIMEOUT in the context's device status
  * word and the kernel returns -- no copy in flight, no tensor memory held -- so the next
  * spec_sync returns SPEC_E_TIMEOUT and the context is spent, while the GPU and other
- * contexts stay usable.  bf16 tensor-core contexts only (SPEC_E_STATE otherwise).
+ * contexts stay usable.  bf16 tensor-core contexts and those with the 8-bit cache (SPEC_E_STATE otherwise).
  * (No counterpart on the pages: the library's own failure reporting.) */
 int spec_check_wait_timeout(spec_ctx* ctx, int budget_ms);
 
@@ -530,7 +530,8 @@ int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int B, int max_
  * [2^-64, 2^120]; value codes of positions below kv_len are not NaN (as spec_kv8_append
  * leaves them).  n_q_heads is a multiple of n_kv_heads, at most 64 per kv head.
  * workspace: spec_kv8_attention_workspace_bytes(...) bytes, 256-byte aligned, contents
- * arbitrary; two calls that overlap on the GPU need one each. */
+ * arbitrary; two calls that overlap on the GPU need one each.  Every wait inside is bounded (2 s);
+ * where one gives up, the rows concerned are NaN, in out and in lse. */
 size_t spec_kv8_attention_workspace_bytes(int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
 int spec_kv8_attention(int num_pages, int n_kv_heads, int head_dim, int B, int max_pages, int n_rows, int n_q_heads,
                        const uint8_t* pool, const float* scales, const int32_t* block_table, const int32_t* row_start,

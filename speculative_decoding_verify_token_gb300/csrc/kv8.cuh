@@ -63,6 +63,7 @@ struct Kv8Attn {
     void* out;              // bf16, row stride o_stride
     long long o_stride;
     float* lse;             // [n_rows][hq] or nullptr
+    int* err;               // status word for a wait that gave up, or nullptr
 };
 
 __device__ __forceinline__ int kv8_row_begin(const Kv8Attn& a, int b) { return a.row_start ? a.row_start[b] : b * a.T; }
@@ -103,6 +104,8 @@ struct Kv8Append {
 cudaError_t kv8_append(const Kv8Append& a, bool f32, int D, cudaStream_t st);
 cudaError_t kv8_attention(const Kv8Attn& a, int D, void* workspace, cudaStream_t st);
 int kv8_attention_kernels(int n_rows, int G);       // kernels that an attention of n_rows rows launches
+// One wait of the attention's on a barrier that nothing completes, reported as one of its own.
+cudaError_t kv8_wait_probe(int* err, int budget_ms, cudaStream_t st);
 
 // Every kernel of the cache is launched so that it may be set up while the one before it in the
 // stream still runs, and waits for that one (griddepcontrol.wait) before it reads or writes anything.

@@ -165,6 +165,20 @@ cudaError_t kv8_attention(const Kv8Attn& a, int D, void* workspace, cudaStream_t
 
 int kv8_attention_kernels(int n_rows, int G) { return may_have_blocks(n_rows, G) ? 3 : 2; }
 
+// (no copy in flight, no tensor memory held)
+__global__ void kv8_wait_probe_kernel(int* err, long long cycles) {
+    __shared__ __align__(8) uint64_t bar;
+    if (threadIdx.x != 0) return;
+    mbar_init(smem_u32(&bar), 1);
+    fence_barrier_init();
+    if (!kv8_wait(bar, 0, cycles)) kv8_report(err);
+}
+
+cudaError_t kv8_wait_probe(int* err, int budget_ms, cudaStream_t st) {
+    kv8_wait_probe_kernel<<<1, 32, 0, st>>>(err, WAIT_CYCLES / 2000 * budget_ms);
+    return cudaGetLastError();
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -197,7 +211,7 @@ extern "C" int spec_kv8_attention(int num_pages, int n_kv_heads, int head_dim, i
     if (!(scale > -INFINITY && scale < INFINITY)) return set_error(SPEC_E_INVAL, "scale is not finite");
     if (n_rows == 0) return SPEC_OK;
     const Kv8Attn a{pool, scales, block_table, num_pages, n_kv_heads, n_q_heads, max_pages, B, B, n_rows, nullptr, row_start,
-                    0, kv_len, 0, q, q_stride, scale, out, o_stride, lse};
+                    0, kv_len, 0, q, q_stride, scale, out, o_stride, lse, nullptr};
     const cudaError_t e = kv8_attention(a, head_dim, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SPEC_OK : set_error(SPEC_E_CUDA, "spec_kv8_attention: %s", cudaGetErrorString(e));
 }

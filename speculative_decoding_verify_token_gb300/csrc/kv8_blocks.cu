@@ -164,9 +164,11 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
             if (!ok) abort_flag = 1;
             if (lane == 0) {          // no copy may still be landing when the block leaves
 #pragma unroll 1
-                for (uint32_t j = kd > KB_NK ? kd - KB_NK : 0; j < kd; ++j) kv8_wait(k_full[j % KB_NK], (j / KB_NK) & 1);
+                for (uint32_t j = kd > KB_NK ? kd - KB_NK : 0; j < kd; ++j)
+                    if (!kv8_wait(k_full[j % KB_NK], (j / KB_NK) & 1)) abort_flag = 1;
 #pragma unroll 1
-                for (uint32_t j = vd > KB_NV ? vd - KB_NV : 0; j < vd; ++j) kv8_wait(c_full[j % KB_NV], (j / KB_NV) & 1);
+                for (uint32_t j = vd > KB_NV ? vd - KB_NV : 0; j < vd; ++j)
+                    if (!kv8_wait(c_full[j % KB_NV], (j / KB_NV) & 1)) abort_flag = 1;
             }
         } else if (warp == 13 || warp == 15) {
             // ---- MMA issuers, one per block of rows.  They take turns, so that the waits of one hide behind
@@ -244,7 +246,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
             if (!ok) abort_flag = 1;
             if (kv8_elect()) mma_commit(smem_u32(&done_bar[blk]));     // nothing may still write tensor memory when it is freed
             __syncwarp();
-            kv8_wait(done_bar[blk], 0);
+            if (!kv8_wait(done_bar[blk], 0)) abort_flag = 1;
         } else if (warp == 14) {
             // ---- factors of the tiles' pages ----
             uint32_t i = 0;
@@ -543,12 +545,13 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
                 if (threadIdx.x == 0) kv8_note(runs[blockIdx.x], s, begun);
                 const int tok = (2 * s.rb + blk) * half + j / G, head = s.h * G + j % G;
                 if (blk < blocks_of(s) && j < half * G && tok < s.n) {
-                    if (s.t0 == 0 && s.t1 == s.tiles)
+                    if (s.t0 == 0 && s.t1 == s.tiles) {
 #pragma unroll 1
                         for (int d = 0; d < D; ++d)
                             static_cast<__nv_bfloat16*>(a.out)[(long long)(s.row0 + tok) * a.o_stride + (size_t)head * D + d] =
                                 __float2bfloat16_rn(__uint_as_float(0x7fc00000u));
-                    else
+                        if (a.lse) a.lse[(size_t)(s.row0 + tok) * a.hq + head] = __uint_as_float(0x7fc00000u);
+                    } else
                         part_ml[(size_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * KB_ROWS + blk * 128 + j] =
                             make_float2(__uint_as_float(0x7fc00000u), 1.0f);
                 }
@@ -559,6 +562,7 @@ kv8_blocks_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0 && abort_flag) kv8_report(a.err);
     if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u) : "memory");
 }
 

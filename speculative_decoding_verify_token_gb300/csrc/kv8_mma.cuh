@@ -36,17 +36,20 @@ template <int D> __device__ __forceinline__ uint64_t kv8_desc_v16(uint32_t addr)
            ((uint64_t)1 << 46);
 }
 
-// Bounded wait for the phase with the given parity: false when WAIT_CYCLES SM clocks (about 2 s)
-// ran out.
+// Bounded wait for the phase with the given parity: false when `cycles` SM clocks (about 2 s) ran out.
 constexpr long long WAIT_CYCLES = 4000000000ll;
-__device__ __forceinline__ bool kv8_wait(uint64_t& bar, uint32_t parity) {
+__device__ __forceinline__ bool kv8_wait(uint64_t& bar, uint32_t parity, long long cycles = WAIT_CYCLES) {
     const uint32_t b = smem_u32(&bar);
     if (mbar_try_wait(b, parity)) return true;
     const long long t0 = clock64();
 #pragma unroll 1
     while (!mbar_try_wait(b, parity))
-        if (clock64() - t0 > WAIT_CYCLES) return false;
+        if (clock64() - t0 > cycles) return false;
     return true;
+}
+// A wait of this block gave up.
+__device__ __forceinline__ void kv8_report(int* err) {
+    if (err) atomicExch(err, SPEC_E_TIMEOUT);
 }
 
 // The same for a converged warp, one answer for all lanes; false too when another role of the

@@ -49,7 +49,7 @@ template <int D> struct KrCfg {
     static constexpr uint32_t QBYTES = 32768;                // hi rows, lo rows; 32 outputs of 256 lanes
     static constexpr int NK = D == 128 ? 3 : 5;              // ring slots of keys,
     static constexpr int NC = D == 128 ? 2 : 5;              // of values as codes
-    static constexpr int NV = D == 128 ? 2 : 4;              // and as fp16
+    static constexpr int NV = D == 128 ? 2 : 4;              // and as fp16 (even: an issuer waits for every phase of its slots)
     static constexpr size_t SMEM = 1024 + 2 * QBYTES + (size_t)(NK + NC + 2 * NV) * TILE;
 };
 
@@ -340,7 +340,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         // no copy may still be landing when the block leaves
         if (lane == 0)
 #pragma unroll 1
-            for (uint32_t j = i > NS ? i - NS : 0; j < i; ++j) kv8_wait(full[j % NS], (j / NS) & 1);
+            for (uint32_t j = i > NS ? i - NS : 0; j < i; ++j)
+                if (!kv8_wait(full[j % NS], (j / NS) & 1)) abort_flag = 1;
     } else if (warp == 10 || warp == 11) {
         // ---- MMA issuers, one per group of softmax warps (tile i belongs to group i % 2).  They take
         // turns, tile by tile, so that the waits of one hide behind the MMAs of the other without
@@ -434,7 +435,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
         if (!ok) abort_flag = 1;
         if (kv8_elect()) mma_commit(smem_u32(&done_bar[g]));     // nothing may still write tensor memory when it is freed
         __syncwarp();
-        kv8_wait(done_bar[g], 0);
+        if (!kv8_wait(done_bar[g], 0)) abort_flag = 1;
     } else {
         // ---- softmax: thread = lane of its group's accumulators ----
         const int grp = warp >> 2, j = (warp & 3) * 32 + lane;
@@ -646,12 +647,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
 #pragma unroll 1
                 for (int q = threadIdx.x; q < s.n * G; q += 256) {
                     const int tt = q / G;
-                    if (s.t0 == 0 && s.t1 == s.tiles)
+                    if (s.t0 == 0 && s.t1 == s.tiles) {
 #pragma unroll 1
                         for (int d = 0; d < D; ++d)
                             static_cast<__nv_bfloat16*>(a.out)[(long long)(s.row0 + tt) * a.o_stride + (size_t)(s.h * G + q - tt * G) * D + d] =
                                 __float2bfloat16_rn(__uint_as_float(0x7fc00000u));
-                    else
+                        if (a.lse) a.lse[(size_t)(s.row0 + tt) * a.hq + s.h * G + q - tt * G] = __uint_as_float(0x7fc00000u);
+                    } else
                         part_ml[part + q] = make_float2(__uint_as_float(0x7fc00000u), 1.0f);
                 }
             } while (walk.next(a, s));
@@ -661,6 +663,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Attn a, float* part_o, float2* part_m
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0 && abort_flag) kv8_report(a.err);
     if (warp == 10) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u) : "memory");
 }
 

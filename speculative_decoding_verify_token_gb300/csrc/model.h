@@ -80,6 +80,7 @@ struct Ctx {
     int kv8_stage = 0;
     void* kv8_out = nullptr;        // [Mmax][hq * hd] bf16: the attention's output
     void* kv8_ws = nullptr;
+    int* kv8_err = nullptr;         // device status word of contexts without tensor-core GEMMs
     int* d_block_table = nullptr;   // [slots][max_pages]
     int* h_block_table = nullptr;   // pinned mirror
     int* d_seq_len = nullptr;       // [slots]

@@ -255,6 +255,7 @@ static int kv8_layer(Ctx& c, int l, const AttnArgs& aa, int B) {
     at.seq_ids = ap.seq_ids; at.T = ap.T; at.kv_len = ap.kv_len; at.kv_add = ap.kv_add;
     at.q = aa.q; at.q_stride = qd; at.scale = aa.scale;
     at.out = aa.o_sw_rows ? c.kv8_out : aa.o; at.o_stride = qd;
+    at.err = aa.err ? aa.err : c.kv8_err;
     cudaError_t e = kv8_append(ap, false, aa.hd, c.stream);
     if (e == cudaSuccess) e = kv8_attention(at, aa.hd, c.kv8_ws, c.stream);
     if (e != cudaSuccess) return cuda_fail("8-bit cache attention", e);
@@ -521,7 +522,7 @@ extern "C" int spec_create_kv(const spec_model_cfg* cfg, const spec_ctx_limits* 
             ok(dalloc(*c, &c->kv8_scales, sizeof(float) * 2 * (size_t)m.n_layers * lim.num_pages * m.n_kv_heads)) &&
             ok(dalloc(*c, &c->kv8_k, 2 * stage_elems)) && ok(dalloc(*c, &c->kv8_v, 2 * stage_elems)) &&
             ok(dalloc(*c, &c->kv8_table, sizeof(int) * (size_t)lim.max_batch * max_pages)) &&
-            ok(dalloc(*c, &c->kv8_out, 2 * (size_t)c->Mmax * qd)) &&
+            ok(dalloc(*c, &c->kv8_out, 2 * (size_t)c->Mmax * qd)) && ok(dalloc(*c, &c->kv8_err, sizeof(int), true)) &&
             ok(dalloc(*c, &c->kv8_ws, spec_kv8_attention_workspace_bytes(c->Mmax, m.n_q_heads, m.n_kv_heads, m.head_dim))))) &&
           ok(dalloc(*c, &c->d_block_table, sizeof(int) * (size_t)lim.max_batch * max_pages, true)) &&
           ok(dalloc(*c, &c->d_seq_len, sizeof(int) * lim.max_batch, true)) &&
@@ -913,12 +914,14 @@ extern "C" int spec_kv_trim(spec_ctx* c, int B, const int32_t* seq_ids, int K, c
 }
 
 // After the stream has been synchronised: SPEC_E_TIMEOUT when a bounded wait inside a
-// tensor-core GEMM gave up since the context was created.  The device word stays set: the
+// tensor-core GEMM or an attention gave up since the context was created.  The device word stays set: the
 // passes since then may hold wrong values, and so may the GEMMs' tile counters, so the
 // context is not to be used again.
 static int device_status(Ctx& c) {
     int word = 0;
-    if (tc_error_word(c, &word) != SPEC_OK) return set_error(SPEC_E_CUDA, "reading the device error word failed");
+    const int rc = c.tc || !c.kv8_err ? tc_error_word(c, &word)
+                   : cudaMemcpy(&word, c.kv8_err, sizeof(int), cudaMemcpyDeviceToHost) == cudaSuccess ? SPEC_OK : SPEC_E_CUDA;
+    if (rc != SPEC_OK) return set_error(SPEC_E_CUDA, "reading the device error word failed");
     if (word != 0)
         return set_error(SPEC_E_TIMEOUT,
                          "a bounded wait on the device gave up (status %d); results since then are unreliable, "
@@ -938,6 +941,10 @@ extern "C" int spec_check_wait_timeout(spec_ctx* c, int budget_ms) {
     clear_error();
     if (!c) return set_error(SPEC_E_INVAL, "ctx is NULL");
     if (budget_ms < 1 || budget_ms > 2000) return set_error(SPEC_E_INVAL, "budget_ms=%d outside [1, 2000]", budget_ms);
+    if (c->kv8_err) {
+        const cudaError_t e = kv8_wait_probe(c->tc ? tc_error_ptr(*c) : c->kv8_err, budget_ms, c->stream);
+        return e == cudaSuccess ? SPEC_OK : cuda_fail("kv8_wait_probe launch", e);
+    }
     return tc_wait_probe(*c, budget_ms);
 }
 

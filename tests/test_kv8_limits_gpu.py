@@ -1,11 +1,14 @@
-"""Calls of the 8-bit cache at the edges of what they accept."""
+"""Calls of the 8-bit cache at the edges of what they accept, and the report of a wait that ran out."""
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
-from tests.test_kv8_gpu import kv8  # noqa: F401  (the fixture)
+import synth
+from tests.test_kv8_gpu import DEV, kv8  # noqa: F401  (the fixture)
+from tests.test_kv8_model_gpu import SIMT1, TC1, i32, lib, make  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -37,3 +40,30 @@ def test_plan_sizes_ascending_in_a_new_process(kv8):  # noqa: F811
     larger one."""
     r = subprocess.run([sys.executable, "-c", PLANS], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("shape", [SIMT1, TC1], ids=["simt", "tc"])
+def test_a_wait_that_runs_out_in_a_context_with_the_cache(lib, shape):  # noqa: F811
+    """The 8-bit attention's waits report to the word that sync reads, with and without tensor-core
+    GEMMs: by the attention's own wait helper on a barrier that nothing completes."""
+    from speculative_decoding_verify_token_gb300 import _lib
+    w = synth.model_weights(shape, seed=0)
+    m = make(lib, shape, w, max_batch=1, max_ctx=64, max_k=4)
+    p = synth.prompt_tokens(1, 20, shape.vocab)
+    m.prefill(0, i32(p[:-1]))
+    m.verify([0], i32(p[-1:]), i32([[0] * 4]), torch.zeros(1, 5, device=DEV), 0.0)
+    m.sync()                                     # nothing has run out
+    for bad in (0, 2001):
+        with pytest.raises(_lib.SpecError) as e:
+            m.check_wait_timeout(bad)
+        assert e.value.code == _lib.SPEC_E_INVAL
+    m.check_wait_timeout(50)
+    for _ in range(2):
+        with pytest.raises(_lib.SpecError) as e:
+            m.sync()
+        assert e.value.code == _lib.SPEC_E_TIMEOUT
+    m.close()
+    m = make(lib, shape, w, max_batch=1, max_ctx=64, max_k=4)
+    m.prefill(0, i32(p[:-1]))
+    m.sync()
+    m.close()
