@@ -478,7 +478,7 @@ void spec_ngram_gate_destroy(spec_ngram_gate* g);
  * Entries outside [0, num_pages) are pages that a sequence does not have: nothing is
  * written to them or read from them, and their keys are masked.
  * Errors: SPEC_E_INVAL for NULL required pointers, sizes below 1 (n_rows, max_rows and
- * free_capacity: below 0), head_dim other than 64 or 128 and misaligned arrays; SPEC_E_RANGE
+ * free_capacity: below 0), head_dim other than 64 or 128, misaligned and overlapping arrays; SPEC_E_RANGE
  * for max_pages above SPEC_KV8_MAX_TOKENS / 16, n_kv_heads above 1024, n_rows above 2^24;
  * SPEC_E_NOMEM for a workspace that is too small; SPEC_E_CUDA on a launch failure.
  * ---------------------------------------------------------------------------------- */
@@ -493,7 +493,7 @@ void spec_ngram_gate_destroy(spec_ngram_gate* g);
  * those of the sequences before it are at most *n_free (one that needs none always passes),
  * and its rows and those before it (of sequences with want <= max_pages) are at most max_rows;
  * one that is not granted gets no page and no row.  Negative lengths count as 0.
- * Outputs (device; none may be an input): block_table [B][max_pages] (in place: the new
+ * Outputs (device; no two arrays of a call may overlap): block_table [B][max_pages] (in place: the new
  * entries held .. want - 1 of each row), row_start [B + 1] (granted rows), kv_len_out [B] =
  * kv_len + granted rows, held_out [B], and per row r < max_rows: slots (int64; page * 16 +
  * offset, -1 behind the last row), positions (0 there), row_seq (-1 there); status [3]: free
@@ -521,7 +521,7 @@ int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int B, int max_
  * (kv head i / (n_q_heads / n_kv_heads)), out = softmax(scale * q . k_j) v_j over the keys
  * j <= kv_len[b] - n + t; a row that sees no key, and the rows behind the last sequence, are
  * zeros.  q and out: bf16, row r, head i at q + r * q_stride + i * head_dim (strides in
- * elements, multiples of 8; 16-byte aligned); lse (may be NULL): float32 [n_rows][n_q_heads],
+ * elements, multiples of 8; 16-byte aligned; out's rows apart from each other); lse (may be NULL): float32 [n_rows][n_q_heads],
  * the natural logarithm of the softmax's denominator, -inf for rows without a key.  Keys and
  * values enter as codes times scale, queries exactly (elements below 2^-13 of a row's largest to
  * within 2^-21 of it), the probabilities times value scale in fp16

@@ -552,8 +552,22 @@ extern "C" int spec_kv8_plan(int B, int max_pages, int max_rows, int free_capaci
     if (!kv_len || !new_len || !held || !n_free || !block_table || !row_start || !kv_len_out || !held_out || !status ||
         (free_capacity > 0 && !free_pages) || (max_rows > 0 && (!slots || !positions || !row_seq)))
         return set_error(SPEC_E_INVAL, "NULL required pointer");
-    if (kv_len_out == kv_len || kv_len_out == new_len || held_out == held || status == n_free)
-        return set_error(SPEC_E_INVAL, "an output is one of the inputs");
+    // blocks read the inputs while others write: nothing may lie over anything else
+    const size_t i4 = sizeof(int32_t), nb = B, nr = max_rows;
+    const struct { const void* p; size_t bytes, align; } arrays[] = {
+        {kv_len, i4 * nb, 4}, {new_len, i4 * nb, 4}, {held, i4 * nb, 4}, {free_pages, i4 * free_capacity, 4}, {n_free, i4, 4},
+        {block_table, i4 * nb * max_pages, 4}, {row_start, i4 * (nb + 1), 4}, {kv_len_out, i4 * nb, 4}, {held_out, i4 * nb, 4},
+        {slots, 8 * nr, 8}, {positions, i4 * nr, 4}, {row_seq, i4 * nr, 4}, {status, i4 * 3, 4}};
+    constexpr int N_IN = 5, N = sizeof(arrays) / sizeof(arrays[0]);
+    for (int i = 0; i < N; ++i) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(arrays[i].p);
+        if (p % arrays[i].align) return set_error(SPEC_E_INVAL, "array %d is not aligned to its type", i);
+        for (int j = 0; i >= N_IN && j < i; ++j) {
+            const uintptr_t q = reinterpret_cast<uintptr_t>(arrays[j].p);
+            if (arrays[i].bytes && arrays[j].bytes && p < q + arrays[j].bytes && q < p + arrays[i].bytes)
+                return set_error(SPEC_E_INVAL, j < N_IN ? "an output is one of the inputs" : "two outputs are the same array");
+        }
+    }
     PlanArgs a{B, max_pages, max_rows, free_capacity, kv_len, new_len, held, free_pages, n_free, block_table, row_start,
                kv_len_out, held_out, reinterpret_cast<long long*>(slots), positions, row_seq, status};
     const int blocks = std::max(1, std::min((max_rows + PLAN_THREADS - 1) / PLAN_THREADS, 152));
@@ -575,6 +589,7 @@ int sv::kv8_cache_checks(int num_pages, int n_kv_heads, int head_dim, int B, int
     if (!block_table || !pool || !scales) return set_error(SPEC_E_INVAL, "NULL required pointer");
     if ((reinterpret_cast<uintptr_t>(pool) & 15) || (reinterpret_cast<uintptr_t>(scales) & 7))
         return set_error(SPEC_E_INVAL, "pool must be 16-byte and scales 8-byte aligned");
+    if (reinterpret_cast<uintptr_t>(block_table) & 3) return set_error(SPEC_E_INVAL, "block_table is not aligned");
     return SPEC_OK;
 }
 
@@ -590,6 +605,8 @@ extern "C" int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int 
     const int al = dtype == SPEC_F32 ? 16 : 8;
     if ((reinterpret_cast<uintptr_t>(k) % al) || (reinterpret_cast<uintptr_t>(v) % al) || k_stride % 4 || v_stride % 4)
         return set_error(SPEC_E_INVAL, "k and v must be aligned to 4 elements, and so must their row strides");
+    if ((reinterpret_cast<uintptr_t>(row_start) | reinterpret_cast<uintptr_t>(kv_len)) & 3)
+        return set_error(SPEC_E_INVAL, "row_start and kv_len must be 4-byte aligned");
     if (n_rows == 0) return SPEC_OK;
     Kv8Append a{pool, scales, block_table, num_pages, n_kv_heads, max_pages, B, B, n_rows, nullptr, row_start, 0,
                  kv_len, 0, k, v, k_stride, v_stride, 0};

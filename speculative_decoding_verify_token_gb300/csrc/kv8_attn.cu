@@ -2,6 +2,7 @@
 // several runs of the work lists share.
 #include <cuda_bf16.h>
 #include <cmath>
+#include <cstdlib>
 
 #include "kv8_mma.cuh"
 
@@ -205,6 +206,10 @@ extern "C" int spec_kv8_attention(int num_pages, int n_kv_heads, int head_dim, i
         return set_error(SPEC_E_INVAL, "NULL required pointer");
     if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15) || q_stride % 8 || o_stride % 8)
         return set_error(SPEC_E_INVAL, "q and out must be 16-byte aligned and their strides multiples of 8");
+    if ((reinterpret_cast<uintptr_t>(row_start) | reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(lse)) & 3)
+        return set_error(SPEC_E_INVAL, "row_start, kv_len and lse must be 4-byte aligned");
+    if (n_rows > 1 && std::llabs(o_stride) < (long long)n_q_heads * head_dim)
+        return set_error(SPEC_E_INVAL, "rows of out overlap: o_stride=%lld", (long long)o_stride);
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return set_error(SPEC_E_INVAL, "workspace not 256-byte aligned");
     if (workspace_bytes < workspace_bytes_of(n_rows, n_q_heads / n_kv_heads, head_dim))
         return set_error(SPEC_E_NOMEM, "workspace of %zu bytes is too small", workspace_bytes);
