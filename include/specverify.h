@@ -505,8 +505,8 @@ int spec_kv8_plan(int B, int max_pages, int max_rows, int free_capacity, const i
                   int32_t* positions, int32_t* row_seq, int32_t* status, void* stream);
 
 /* Quantise new keys and values into the cache.  k, v (device, dtype SPEC_F32 or SPEC_BF16):
- * row r, head h at k + r * k_stride + h * head_dim (strides in elements; base and strides
- * aligned to 4 elements).  Every page that gets a token is written whole: per head and side
+ * row r, head h at k + r * k_stride + h * head_dim (strides in elements; base and, of more than
+ * one row, strides aligned to 4 elements).  Every page that gets a token is written whole: per head and side
  * the scale 2^e, e the smallest integer >= -64 with amax <= 448 * 2^e over the tokens that it
  * keeps (positions before the new ones, at their old codes and scale) and the new ones; codes
  * round to nearest even of x / 2^e; zeros behind the last token.  Kept codes are re-scaled
@@ -521,7 +521,7 @@ int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int B, int max_
  * (kv head i / (n_q_heads / n_kv_heads)), out = softmax(scale * q . k_j) v_j over the keys
  * j <= kv_len[b] - n + t; a row that sees no key, and the rows behind the last sequence, are
  * zeros.  q and out: bf16, row r, head i at q + r * q_stride + i * head_dim (strides in
- * elements, multiples of 8; 16-byte aligned; out's rows apart from each other); lse (may be NULL): float32 [n_rows][n_q_heads],
+ * elements, of more than one row multiples of 8; 16-byte aligned; out's rows apart from each other); lse (may be NULL): float32 [n_rows][n_q_heads],
  * the natural logarithm of the softmax's denominator, -inf for rows without a key.  Keys and
  * values enter as codes times scale, queries exactly (elements below 2^-13 of a row's largest to
  * within 2^-21 of it), the probabilities times value scale in fp16

@@ -603,7 +603,7 @@ extern "C" int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int 
     if (dtype != SPEC_F32 && dtype != SPEC_BF16) return set_error(SPEC_E_INVAL, "dtype=%d", dtype);
     if (!row_start || !kv_len || (n_rows > 0 && (!k || !v))) return set_error(SPEC_E_INVAL, "NULL required pointer");
     const int al = dtype == SPEC_F32 ? 16 : 8;
-    if ((reinterpret_cast<uintptr_t>(k) % al) || (reinterpret_cast<uintptr_t>(v) % al) || k_stride % 4 || v_stride % 4)
+    if ((reinterpret_cast<uintptr_t>(k) % al) || (reinterpret_cast<uintptr_t>(v) % al) || (n_rows > 1 && (k_stride % 4 || v_stride % 4)))
         return set_error(SPEC_E_INVAL, "k and v must be aligned to 4 elements, and so must their row strides");
     if ((reinterpret_cast<uintptr_t>(row_start) | reinterpret_cast<uintptr_t>(kv_len)) & 3)
         return set_error(SPEC_E_INVAL, "row_start and kv_len must be 4-byte aligned");

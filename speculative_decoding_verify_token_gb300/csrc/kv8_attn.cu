@@ -204,7 +204,7 @@ extern "C" int spec_kv8_attention(int num_pages, int n_kv_heads, int head_dim, i
                          n_q_heads, n_kv_heads);
     if (!row_start || !kv_len || (n_rows > 0 && (!q || !out)) || !workspace)
         return set_error(SPEC_E_INVAL, "NULL required pointer");
-    if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15) || q_stride % 8 || o_stride % 8)
+    if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15) || (n_rows > 1 && (q_stride % 8 || o_stride % 8)))
         return set_error(SPEC_E_INVAL, "q and out must be 16-byte aligned and their strides multiples of 8");
     if ((reinterpret_cast<uintptr_t>(row_start) | reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(lse)) & 3)
         return set_error(SPEC_E_INVAL, "row_start, kv_len and lse must be 4-byte aligned");

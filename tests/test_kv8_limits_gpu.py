@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import synth
-from tests.test_kv8_gpu import DEV, kv8  # noqa: F401  (the fixture)
+from tests.test_kv8_gpu import DEV, ints, kv8  # noqa: F401  (the fixture)
 from tests.test_kv8_model_gpu import SIMT1, TC1, i32, lib, make  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -40,6 +40,23 @@ def test_plan_sizes_ascending_in_a_new_process(kv8):  # noqa: F811
     larger one."""
     r = subprocess.run([sys.executable, "-c", PLANS], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr[-2000:]
+
+
+def test_one_row_of_any_stride(kv8):  # noqa: F811
+    """With one row its stride means nothing, and torch gives such a dimension any."""
+    g = torch.Generator(device=DEV).manual_seed(0)
+    hq, hkv, D = 4, 2, 64
+    wide = torch.randn(2, hq * D + 2 * hkv * D + 3, generator=g, device=DEV).bfloat16()
+    q = wide[:, :hq * D].view(2, hq, D)[:1]
+    k, v = (wide[:, (hq + i * hkv) * D:(hq + (i + 1) * hkv) * D].view(2, hkv, D)[:1] for i in (0, 1))
+    out = torch.empty(2, hq * D + 3, dtype=torch.bfloat16, device=DEV)[:, :hq * D].view(2, hq, D)[:1]
+    assert all(t.stride(0) % 4 == 3 for t in (q, k, v, out))
+    pool, scales = kv8.new_cache(1, hkv, D)
+    table, rs, kv = ints([[0]]), ints([0, 1]), ints([1])
+    kv8.append(pool, scales, table, rs, kv, k, v)
+    kv8.attention(q, pool, scales, table, rs, kv, out=out)
+    want = v.repeat_interleave(hq // hkv, 1).float()
+    assert ((out.float() - want).abs() <= 2.0 ** -3 * want.abs() + 2.0 ** -8).all()      # e4m3: half a step is 2^-4
 
 
 @pytest.mark.parametrize("shape", [SIMT1, TC1], ids=["simt", "tc"])
