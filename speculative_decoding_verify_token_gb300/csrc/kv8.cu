@@ -278,18 +278,16 @@ __global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 2 ? 4 : 2) kv8_ap
                 }
                 seq = lo;
                 row0 = a.row_start[lo];
-                first = row0 - a.row_start[lo + 1];
+                len = a.kv_len[lo];
+                first = row0 - a.row_start[lo + 1] + len;
+                pos = first + r - row0;
             }
         } else if (r < a.B * a.T) {
-            seq = r / a.T;
-            row0 = seq * a.T;
-            first = -a.T;
-        }
-        if (seq >= 0) {
-            seq = a.seq_ids ? a.seq_ids[seq] : seq;
+            row0 = r / a.T * a.T;
+            seq = a.seq_ids ? a.seq_ids[r / a.T] : r / a.T;
             if (seq >= 0 && seq < a.n_tables) {
                 len = a.kv_len[seq] + a.kv_add;
-                first += len;
+                first = len - a.T;
                 pos = first + r - row0;
             }
         }

@@ -82,7 +82,8 @@ __device__ __forceinline__ void kv8_sequence(const Kv8Attn& a, int b, int& slot,
     }
 }
 
-// What the append reads and writes; sequences, rows and lengths as above.
+// What the append reads and writes; rows and lengths as above, but with row_start the sequences are the
+// rows of the block table (seq_ids and kv_add are for batches of T rows each).
 struct Kv8Append {
     uint8_t* pool;
     float* scales;
