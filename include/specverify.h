@@ -212,9 +212,13 @@ int spec_create(const spec_model_cfg* cfg, const spec_ctx_limits* limits, void* 
  * spec_create.  SPEC_KV_E4M3 (bf16 models, head_dim 64 or 128, at most 64 query heads per kv
  * head, else SPEC_E_INVAL): the 8-bit paged cache described below, a pool per layer; every
  * pass appends and attends as spec_kv8_append and spec_kv8_attention do.  Half the bytes of a
- * bf16 cache, and with it other bits: a token's keys share a scale with those of its page, and
+ * bf16 cache, and with it other bits: queries and the attention's output are rounded to bf16
+ * once (their lo halves are not used), a token's keys share a scale with those of its page, and
  * attention splits its keys by the batch, so that a token's logits can depend in their last
- * bits on the batch and on drafts that were trimmed from its page. */
+ * bits on the batch.  A pass appends its drafts before it knows which are accepted: a draft
+ * with larger elements than its page raises the page's scale, and what the tokens kept there
+ * lose by it (they become multiples of 2^-9 of that scale, whole elements zero where the draft
+ * is far larger) they do not get back when the draft is trimmed. */
 #define SPEC_KV_MODEL 0
 #define SPEC_KV_E4M3 1
 int spec_create_kv(const spec_model_cfg* cfg, const spec_ctx_limits* limits, int kv, void* stream, spec_ctx** out);

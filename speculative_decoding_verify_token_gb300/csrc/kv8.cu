@@ -9,7 +9,8 @@
 // and a scale only moves its range, and it makes re-scaling exact: when new tokens move a
 // page's scale, the kept codes only change their exponent (bits are lost only where a code
 // falls into the subnormal range).  The scale is a function of the page's tokens alone, so a
-// page that held rejected drafts gets back the scale it would have had without them.
+// page that held rejected drafts gets back the scale it would have had without them, but not the
+// bits of kept codes that fell below the smallest step of a larger draft's scale.
 #include <algorithm>
 
 #include <cuda_bf16.h>

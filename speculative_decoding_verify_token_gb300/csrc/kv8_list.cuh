@@ -68,7 +68,8 @@ __device__ __forceinline__ int kb_keys(int n, int len, int tb, int rb) {
     return max(0, (int)min((long long)len, (long long)len - n + (long long)tb * (rb + 1)));
 }
 
-// Sum of floor((a i + b) / 128) for i < n (a, b >= 0), by the Euclidean recursion on (a, 128).
+// Sum of floor((a i + b) / 128) for i < n (a, b >= 0), by the Euclidean recursion on (a, 128): the steps
+// are those of the floor sum in public algorithm libraries (the AtCoder Library, CC0).
 // n a + b stays below 2^32: a call has at most 2^24 rows, so n a does by 2^24 tokens.
 __device__ __forceinline__ long long kv8_floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     uint32_t m = KV8_TILE;
