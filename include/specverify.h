@@ -480,7 +480,9 @@ void spec_ngram_gate_destroy(spec_ngram_gate* g);
  * sequence b with its new rows, which are its last ones.  Every length lives on the
  * device, so all three calls can be captured in a CUDA graph and replayed as they change.
  * Entries outside [0, num_pages) are pages that a sequence does not have: nothing is
- * written to them or read from them, and their keys are masked.
+ * written to them or read from them, and their keys are masked.  A kv_len past the table's
+ * 16 max_pages positions is a mistake that harms nothing else: what lies beyond is not appended, and
+ * attention takes the length as 16 max_pages.
  * Errors: SPEC_E_INVAL for NULL required pointers, sizes below 1 (n_rows, max_rows and
  * free_capacity: below 0), head_dim other than 64 or 128, misaligned and overlapping arrays; SPEC_E_RANGE
  * for max_pages above SPEC_KV8_MAX_TOKENS / 16, n_kv_heads above 1024, n_rows above 2^24;

@@ -283,7 +283,10 @@ template <int D> __device__ __forceinline__ void kv8_widen16(uint4 w, uint8_t* d
 // lets it start only when the kernels before the call are done.  It is done itself only
 // when the first is, so that the join waits for both.
 __device__ __forceinline__ void kv8_begin(bool after) {
-    if (!after) pdl_wait();
+    // (the second reads what the kernels before the call wrote without a wait of its own: no line of
+    // them may be left in this SM's L1 from before)
+    if (after) __threadfence();
+    else pdl_wait();
     pdl_launch_dependents();
 }
 __device__ __forceinline__ void kv8_finish(bool after) {
