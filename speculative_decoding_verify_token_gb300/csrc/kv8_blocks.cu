@@ -1,7 +1,7 @@
 // Causal attention over the 8-bit paged cache for sequences of more than 128 query rows per kv
 // head (prompt chunks).  Bound by the tensor cores' 1,024 clocks for the products of 128 rows and
 // 128 keys, against 256 bytes of cache per key, and, as measured, by the row threads: 2,048 rows of
-// 8,192 keys take 237 us (52% of the bf16 rate), the tensor pipe 45% and the issue slots 49%
+// 8,192 keys take 240 us (52% of the bf16 rate), the tensor pipe 44% and the issue slots 49%
 // busy; a tile of 256 rows takes 3,800 clocks, of which a thread's 128 keys are 3,100.
 //
 // A group is 2 x floor(128 / G) tokens of one sequence and kv head: two blocks of up to 128

@@ -36,7 +36,7 @@ __device__ __forceinline__ int kr_tiles(const Kv8Attn& a, int b, int& slot, int&
 // Units (of some 0.2 us) of a tile and of the rest of a group of R rows, mostly the wait for its queries.  Batches of
 // 32 sequences to 16k, D = 128: a tile takes 0.84, 0.98 and 1.4 us, the rest of a group 4.4, 6.2 and 8.1 to 9.3;
 // 48 sequences to 8k, D = 64: 0.7, 0.96 and 1.2, and 2.7 to 3.2.  The extras are those whose runs end closest to
-// each other (32 verify passes: 152 us with 12, 22 and 26 for both, 142 with these; 48 decodes 80 and 72).
+// each other (32 verify passes: 152 us with 12, 22 and 26 for both, 143 with these; 48 decodes 80 and 73).
 __device__ __forceinline__ int kr_weight(int R) { return R <= 32 ? 4 : (R <= 64 ? 5 : 6); }
 template <int D> __device__ __forceinline__ int kr_extra(int R) {
     return D == 64 ? (R <= 32 ? 18 : (R <= 64 ? 26 : 32)) : (R <= 32 ? 24 : (R <= 64 ? 36 : 46));

@@ -22,9 +22,9 @@
 // run's part of a group the copies and both outputs are added through shared memory.
 // What it replaced (32 verify passes of up to 16k keys): the running maximum of every tile over
 // lanes that held keys, 580 us; a vote per tile instead, 212 us, bound by the latency of some 4,600 warp
-// instructions a tile.  Now 142 us for those (70% of the copy rate),
-// 61 us for 5 rows of 128k keys, 72 us for 48 decodes of D = 64; with two-term e4m3 probabilities, whose products
-// need no widened values, 136, 59 and 76.
+// instructions a tile.  Now 143 us for those (70% of the copy rate, the tensor
+// pipe 51% and the issue slots 37% busy), 62 us for 5 rows of 128k keys, 74 us for 48 decodes of D = 64; with two-term e4m3 probabilities, whose products
+// need no widened values, 135, 59 and 76.
 // Warps: 0-3 and 4-7 softmax, 8 copies keys, 9 copies values and writes the pages' factors, 10 and
 // 11 issue the MMAs of the two groups, 12-15 widen values and prepare the queries of the next group of rows.
 #include <cuda_bf16.h>
