@@ -553,18 +553,21 @@ extern "C" int spec_kv8_plan(int B, int max_pages, int max_rows, int free_capaci
         return set_error(SPEC_E_INVAL, "NULL required pointer");
     // blocks read the inputs while others write: nothing may lie over anything else
     const size_t i4 = sizeof(int32_t), nb = B, nr = max_rows;
-    const struct { const void* p; size_t bytes, align; } arrays[] = {
-        {kv_len, i4 * nb, 4}, {new_len, i4 * nb, 4}, {held, i4 * nb, 4}, {free_pages, i4 * free_capacity, 4}, {n_free, i4, 4},
-        {block_table, i4 * nb * max_pages, 4}, {row_start, i4 * (nb + 1), 4}, {kv_len_out, i4 * nb, 4}, {held_out, i4 * nb, 4},
-        {slots, 8 * nr, 8}, {positions, i4 * nr, 4}, {row_seq, i4 * nr, 4}, {status, i4 * 3, 4}};
+    const struct { const char* name; const void* p; size_t bytes, align; } arrays[] = {
+        {"kv_len", kv_len, i4 * nb, 4}, {"new_len", new_len, i4 * nb, 4}, {"held", held, i4 * nb, 4},
+        {"free_pages", free_pages, i4 * free_capacity, 4}, {"n_free", n_free, i4, 4},
+        {"block_table", block_table, i4 * nb * max_pages, 4}, {"row_start", row_start, i4 * (nb + 1), 4},
+        {"kv_len_out", kv_len_out, i4 * nb, 4}, {"held_out", held_out, i4 * nb, 4}, {"slots", slots, 8 * nr, 8},
+        {"positions", positions, i4 * nr, 4}, {"row_seq", row_seq, i4 * nr, 4}, {"status", status, i4 * 3, 4}};
     constexpr int N_IN = 5, N = sizeof(arrays) / sizeof(arrays[0]);
     for (int i = 0; i < N; ++i) {
         const uintptr_t p = reinterpret_cast<uintptr_t>(arrays[i].p);
-        if (p % arrays[i].align) return set_error(SPEC_E_INVAL, "array %d is not aligned to its type", i);
+        if (p % arrays[i].align) return set_error(SPEC_E_INVAL, "%s is not aligned to its type", arrays[i].name);
         for (int j = 0; i >= N_IN && j < i; ++j) {
             const uintptr_t q = reinterpret_cast<uintptr_t>(arrays[j].p);
             if (arrays[i].bytes && arrays[j].bytes && p < q + arrays[j].bytes && q < p + arrays[i].bytes)
-                return set_error(SPEC_E_INVAL, j < N_IN ? "an output is one of the inputs" : "two outputs are the same array");
+                return set_error(SPEC_E_INVAL, "%s: %s and %s", j < N_IN ? "an output is one of the inputs" : "two outputs are the same array",
+                                 arrays[i].name, arrays[j].name);
         }
     }
     PlanArgs a{B, max_pages, max_rows, free_capacity, kv_len, new_len, held, free_pages, n_free, block_table, row_start,

@@ -3,10 +3,12 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 import synth
+from tests import test_kv8_gpu as base
 from tests.test_kv8_gpu import DEV, ints, kv8  # noqa: F401  (the fixture)
 from tests.test_kv8_model_gpu import SIMT1, TC1, i32, lib, make  # noqa: F401  (the fixture)
 
@@ -57,6 +59,29 @@ def test_one_row_of_any_stride(kv8):  # noqa: F811
     kv8.attention(q, pool, scales, table, rs, kv, out=out)
     want = v.repeat_interleave(hq // hkv, 1).float()
     assert ((out.float() - want).abs() <= 2.0 ** -3 * want.abs() + 2.0 ** -8).all()      # e4m3: half a step is 2^-4
+
+
+@pytest.mark.parametrize("n", [3, 150])
+def test_rows_of_nobody_and_rows_without_a_number(kv8, n):  # noqa: F811
+    """Rows in front of the first sequence are zeros like those behind the last; a NaN or an infinity in a
+    query makes its own rows NaN and no others."""
+    rng = np.random.default_rng(n)
+    hq, hkv, D = 8, 2, 64
+    rs, kv, table, pool, scales = base.make_cache(rng, [(n, 333), (2, 40)], hkv, D)
+    rs = rs + 2
+    q = torch.from_numpy(rng.standard_normal((int(rs[-1]) + 2, hq, D))).to(torch.bfloat16)
+    base.check_attention(kv8, q, pool, scales, table, rs, kv)
+    pd, sd = torch.from_numpy(pool).to(DEV), torch.from_numpy(scales).to(DEV)
+    args = (pd, sd, ints(table), ints(rs), ints(kv))
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = kv8.attention(q.to(DEV), *args, lse=lse)
+    q[3, 5, 7], q[4, 1, 0], q[int(rs[1]), 0, 63] = float("nan"), float("inf"), float("-inf")
+    lse2 = torch.empty(q.shape[:2], device=DEV)
+    out2 = kv8.attention(q.to(DEV), *args, lse=lse2)
+    bad = torch.isnan(q.float()).any(-1).to(DEV) | torch.isinf(q.float()).any(-1).to(DEV)
+    assert int(bad.sum()) == 3
+    assert torch.isnan(out2[bad]).all() and torch.isnan(lse2[bad]).all()
+    assert torch.equal(out2[~bad], out[~bad]) and torch.equal(lse2[~bad], lse[~bad])
 
 
 @pytest.mark.parametrize("shape", [SIMT1, TC1], ids=["simt", "tc"])
