@@ -532,7 +532,7 @@ int spec_kv8_append(int num_pages, int n_kv_heads, int head_dim, int B, int max_
  * values enter as codes times scale, queries exactly (elements below 2^-13 of a row's largest to
  * within 2^-21 of it), the probabilities times value scale in fp16
  * (11 bits, to within 2^-37 of the row's largest, above 128 rows per kv head of a sequence
- * 2^-32); sums and softmax statistics are fp32.  Scales are positive, in
+ * 2^-32); scores, sums and softmax statistics are fp32 (scores past its range make a row NaN).  Scales are positive, in
  * [2^-64, 2^120]; value codes of positions below kv_len are not NaN (as spec_kv8_append
  * leaves them).  n_q_heads is a multiple of n_kv_heads, at most 64 per kv head.
  * workspace: spec_kv8_attention_workspace_bytes(...) bytes, 256-byte aligned, contents
